@@ -16,7 +16,8 @@
  *   - All matrix pointers are DEVICE pointers owned by the caller; the library
  *     allocates no device memory, keeps no state between calls (beyond cached
  *     device attributes and a thread-local error string) and needs no
- *     workspace.  Matrix pointers must be 16-byte aligned.
+ *     workspace, except mixq_kv4_attention, which is given one.  Matrix
+ *     pointers must be 16-byte aligned.
  *   - fp16 data is IEEE binary16, passed as void*.  Matrices are row-major.
  *   - Every call is asynchronous on `stream` (a cudaStream_t passed as void*;
  *     NULL = the legacy default stream).  Errors a host can see (bad sizes,
@@ -310,6 +311,126 @@ size_t mixq_gemm_workspace_size(int M, int N, int K);
  */
 mixq_status mixq_gemm_plan(int mode, int M, int N, int K, int num_sms, int *bn, int *split,
                            int *ctas);
+
+/*
+ * ------------------------------------------------------------- 4-bit KV cache
+ * The KV4 part of W4A8KV4 (QServe notes, W4A8KV4: weights in 4, activations in
+ * 8 and the key/value cache in 4 bits): K and V rows are quantized as they are
+ * written into a paged cache, and attention reads the 4-bit codes.  Each row of
+ * one token and kv head (head_dim values) is its own asymmetric group:
+ *   lo = min x, hi = max x, s = T((hi - lo) / 15),
+ *   c = min(rint((x - lo) * (1 / s)), 15),  the row stands for c * s + lo
+ * with T the cache's 16-bit type, the differences, the product and 1/s in fp32,
+ * each rounded once, rint half to even, and c = 0 where s is 0 (a constant row;
+ * also a bf16 s below 2^-126).  A row that holds a NaN or an infinity, or whose
+ * hi - lo is not finite in fp32, gets s = lo = NaN and so stands for NaN.
+ *
+ * Layout.  A page holds page_size tokens (a positive multiple of 16) of every kv
+ * head: [n_kv_heads][page_size / 16] records, page_size * (head_dim + 8) bytes a
+ * head.  A record is 16 tokens of one kv head, D = head_dim:
+ *   offset 0      K codes [16][D/2]; in each 4-byte word (8 dims 8w..8w+7) nibble p
+ *                 holds dim 8w+2p and nibble p+4 holds dim 8w+2p+1, p = 0..3
+ *   offset 8 D    V codes; byte column b (dims 2b in the low and 2b+1 in the high
+ *                 nibble) of token 2t + i/2 + 8(i%2) at
+ *                 (b/32)*512 + (b%8)*64 + t*16 + (b/8%4)*4 + i, t = 0..3, i = 0..3
+ *   offset 16 D   (s, lo) of K, 16 pairs of T;  offset 16 D + 64: those of V
+ * Position j of sequence s is token j % page_size of page
+ * table[s*table_stride + j / page_size].
+ *
+ * mixq_kv4_cache describes a cache (host struct, device memory owned by the
+ * caller): pages 16-byte aligned, page_stride the bytes from one page to the
+ * next (a multiple of 16, at least n_kv_heads * mixq_kv4_page_bytes, so that
+ * the layers of a model may share one pool), head_dim 64 or 128, dtype
+ * MIXQ_KV4_F16 or MIXQ_KV4_BF16 (type of K, V, q, out and of the pairs).
+ *
+ * The calls take a batch of n_seqs sequences.  Rows (tokens) of the batch lie
+ * one after another: those of sequence s are [cu[s], cu[s+1]) of n_rows; cu NULL
+ * means one row per sequence (n_rows == n_seqs).  Rows behind cu[n_seqs] are
+ * neither read nor written.  table int32 [n_seqs][table_width], cu int32
+ * [n_seqs + 1], the other per-sequence arrays int32 [n_seqs], all on the
+ * device: a call can be captured once and replayed as the lengths change.  The
+ * device reports MIXQ_ERR_INVALID_ARG in *status for a page number outside
+ * [0, n_pages) or beyond table_width (those tokens are not stored, read back as
+ * they were, and are hidden from attention) and for a cu that falls or leaves
+ * [0, n_rows] (such a sequence counts as empty).  Table entries that no
+ * position in use needs are not read.
+ */
+enum { MIXQ_KV4_F16 = 0, MIXQ_KV4_BF16 = 1 };
+
+typedef struct mixq_kv4_cache {
+  void *pages;
+  int64_t page_stride;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+} mixq_kv4_cache;
+
+/* Bytes of one kv head in a page, page_size * (head_dim + 8); 0 if unsupported. */
+size_t mixq_kv4_page_bytes(int page_size, int head_dim);
+
+/*
+ * Quantize new rows into the cache.  seq_lens[s] is the length of sequence s
+ * WITH its new rows: row cu[s] + i goes to position seq_lens[s] - n + i, with n =
+ * cu[s+1] - cu[s]; rows whose position would be negative are skipped (a padded
+ * entry of a batch has seq_lens 0).  k, v [n_rows][n_kv_heads][head_dim], strides
+ * in elements, multiples of 8; 16-byte aligned.  Other tokens of the touched
+ * records keep their bytes.  Two rows of one call must not name the same
+ * place (a page twice in the written part of the table).
+ */
+mixq_status mixq_kv4_append(const mixq_kv4_cache *cache, const void *k, int64_t k_row,
+                            int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
+                            int n_seqs, int n_rows, const int32_t *table, int table_width,
+                            int64_t table_stride, const int32_t *seq_lens, const int32_t *cu,
+                            int32_t *status, void *stream);
+
+/*
+ * Read rows back: row cu[s] + i of k_out and v_out receives T(c * s + lo) of
+ * position first[s] + i of sequence s (first NULL: from position 0), computed in
+ * fp32 and rounded once; a value above T's largest finite one (s is rounded)
+ * becomes that.  Shapes and strides as in mixq_kv4_append.  Rows at negative
+ * positions stay as they were.
+ */
+mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_row,
+                          int64_t k_head, void *v_out, int64_t v_row, int64_t v_head,
+                          int n_seqs, int n_rows, const int32_t *table, int table_width,
+                          int64_t table_stride, const int32_t *first, const int32_t *cu,
+                          int32_t *status, void *stream);
+
+/*
+ * Attention of new tokens over the cache.  Query row cu[s] + i of sequence s has
+ * position p = seq_lens[s] - n + i (its own K and V are in the cache already);
+ * query head h reads kv head h / (n_q_heads / n_kv_heads):
+ *   key j is visible when j <= p and (window == 0 or j > p - window or j < sinks)
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * (q . k_j) - max)
+ * over the visible keys, k_j and v_j the rows c * s + lo unrounded, scores, sums
+ * and products in fp32, weights times V's scale in fp16 under a power of two.  A
+ * row that sees no key is written as zeros.  The codes enter the products as they
+ * are; a NaN in a row reaches only those queries that see the row.
+ *   q, out   [n_rows][n_q_heads][head_dim], strides in elements, multiples of 8;
+ *            16-byte aligned; out must not overlap q
+ *   max_new  a bound on cu[s+1] - cu[s], or 0 for none: it picks the kernel, the
+ *            results are right whatever it says
+ *   window >= 0 (0: no window), sinks >= 0 (first tokens that stay visible)
+ *   work     device scratch of mixq_kv4_attention_workspace_size bytes, 16-byte
+ *            aligned; its contents before and after mean nothing, and calls that
+ *            may overlap on the GPU must not share it
+ * One sequence's keys may be joined from several partial sums; which, depends
+ * only on the lengths and the shape, so equal calls give equal bits.
+ */
+mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64_t q_row,
+                               int64_t q_head, void *out, int64_t o_row, int64_t o_head,
+                               int n_q_heads, int n_seqs, int n_rows, int max_new,
+                               const int32_t *table, int table_width, int64_t table_stride,
+                               const int32_t *seq_lens, const int32_t *cu, float scale,
+                               int window, int sinks, void *work, size_t work_bytes,
+                               int32_t *status, void *stream);
+
+/* Bytes of `work` for any call with this head_dim on a device of num_sms SMs
+ * (num_sms <= 0: the current device; 0 if there is none or head_dim is not
+ * supported).  It does not grow with the batch or the lengths. */
+size_t mixq_kv4_attention_workspace_size(int head_dim, int num_sms);
 
 /*
  * Test-only: the gemm mainloop alone, raw INT32 accumulators out

@@ -7,7 +7,9 @@ no CPU fallback.
 
 Low-level calls keep the C names (``mixq_quantize_act`` ...) and take torch
 tensors; :class:`PackedWeights`, :func:`prepack`, :func:`quantize_act`,
-:func:`gemm` and :func:`linear` are thin conveniences over them.
+:func:`gemm` and :func:`linear` are thin conveniences over them.  The 4-bit KV
+cache is :class:`KV4Cache` with :func:`kv4_append`, :func:`kv4_read` and
+:func:`kv4_attention`.
 """
 from __future__ import annotations
 
@@ -23,9 +25,20 @@ STATUS = {0: "MIXQ_OK", 1: "MIXQ_ERR_INVALID_ARG", 2: "MIXQ_ERR_UNSUPPORTED_SHAP
           3: "MIXQ_ERR_MISALIGNED", 4: "MIXQ_ERR_CUDA", 5: "MIXQ_ERR_TIMEOUT",
           6: "MIXQ_ERR_NO_DEVICE"}
 GROUP = 128
+MIXQ_KV4_F16, MIXQ_KV4_BF16 = 0, 1
 
 _c = ctypes
 _VP, _I, _F, _SZ, _U64 = _c.c_void_p, _c.c_int, _c.c_float, _c.c_size_t, _c.c_uint64
+_L = _c.c_int64
+
+
+class _KV4Desc(_c.Structure):
+    """struct mixq_kv4_cache"""
+    _fields_ = [("pages", _VP), ("page_stride", _L), ("n_pages", _c.c_int32),
+                ("page_size", _c.c_int32), ("n_kv_heads", _c.c_int32), ("head_dim", _c.c_int32),
+                ("dtype", _c.c_int32)]
+
+
 _SIGNATURES = {
     "mixq_last_error": (_c.c_char_p, []),
     "mixq_version": (_I, []),
@@ -46,6 +59,13 @@ _SIGNATURES = {
                                     _VP, _VP]),
     "mixq_gemm_workspace_size": (_SZ, [_I, _I, _I]),
     "mixq_gemm_plan": (_I, [_I, _I, _I, _I, _I, _c.POINTER(_I), _c.POINTER(_I), _c.POINTER(_I)]),
+    "mixq_kv4_page_bytes": (_SZ, [_I, _I]),
+    "mixq_kv4_append": (_I, [_VP, _VP, _L, _L, _VP, _L, _L, _I, _I, _VP, _I, _L, _VP, _VP, _VP,
+                             _VP]),
+    "mixq_kv4_read": (_I, [_VP, _VP, _L, _L, _VP, _L, _L, _I, _I, _VP, _I, _L, _VP, _VP, _VP, _VP]),
+    "mixq_kv4_attention": (_I, [_VP, _VP, _L, _L, _VP, _L, _L, _I, _I, _I, _I, _VP, _I, _L, _VP,
+                                _VP, _F, _I, _I, _VP, _SZ, _VP, _VP]),
+    "mixq_kv4_attention_workspace_size": (_SZ, [_I, _I]),
     "mixq_debug_gemm_i32": (_I, [_I, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _I, _VP, _VP]),
     "mixq_debug_max_active_clusters": (_I, [_I, _I, _I, _I, _c.POINTER(_I)]),
     "mixq_debug_unpack_w8": (_I, [_I, _I, _VP, _VP, _VP]),
@@ -387,3 +407,194 @@ def linear(X, w: PackedWeights, threshold: float = 6.0, status=None, stream=None
     """Y = MixQ layer(X) for fp16 X [M, K] on the device: quantize, then GEMM."""
     q = quantize_act(X, w.idx, threshold, status=status, stream=stream)
     return gemm(q, w, status=status, stream=stream), q
+
+
+# ------------------------------------------------------------ 4-bit KV cache
+class KV4Cache:
+    """A paged cache of K and V rows in 4 bits (layout: mixq_kv4_cache in mixq.h).
+
+    pages: uint8 [n_pages, n_kv_heads, page_size * (head_dim + 8)] on the device; pages may
+    lie further apart than their size (``pool[:, layer]`` of a pool shared by the layers).
+    dtype (torch.float16 or torch.bfloat16) is the type of the rows written, read and attended
+    with.  Sequences find their pages through a block table given to each call."""
+
+    def __init__(self, pages, page_size: int, head_dim: int, dtype=None):
+        import torch
+        dtype = torch.float16 if dtype is None else dtype
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise MixqError(1, f"cache dtype {dtype} must be torch.float16 or torch.bfloat16")
+        if pages.dtype != torch.uint8 or pages.dim() != 3:
+            raise MixqError(1, "pages must be a uint8 tensor [n_pages, n_kv_heads, page bytes]")
+        per = page_size * (head_dim + 8)
+        if pages.shape[2] != per or (pages.numel() and (
+                pages.stride(2) != 1 or (pages.shape[1] > 1 and pages.stride(1) != per))):
+            raise MixqError(1, f"a kv head's part of a page must be {per} contiguous bytes, the "
+                               "heads of a page one after another")
+        self.pages, self.page_size, self.head_dim, self.dtype = pages, page_size, head_dim, dtype
+        self.n_kv_heads = pages.shape[1]
+        stride = pages.stride(0) if pages.shape[0] > 1 else max(1, pages.shape[1]) * per
+        self._desc = _KV4Desc(pages.data_ptr(), stride, pages.shape[0], page_size, pages.shape[1],
+                              head_dim, MIXQ_KV4_F16 if dtype == torch.float16 else MIXQ_KV4_BF16)
+        self._ref = ctypes.addressof(self._desc)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int = 128, page_size: int = 64,
+              dtype=None, device=None) -> "KV4Cache":
+        """A cache with its own pages (zeroed: they stand for zeros)."""
+        torch = _require_cuda()
+        pages = torch.zeros((n_pages, n_kv_heads, page_size * (head_dim + 8)), dtype=torch.uint8,
+                            device=device or "cuda")
+        return cls(pages, page_size, head_dim, dtype)
+
+
+def _kv4_rows(cache: KV4Cache, name: str, t, heads=None):
+    if t.dtype != cache.dtype or t.dim() != 3 or t.shape[2] != cache.head_dim or (
+            heads is not None and t.shape[1] != heads):
+        raise MixqError(1, f"{name} must be {cache.dtype} [rows, "
+                           f"{'heads' if heads is None else heads}, {cache.head_dim}], not "
+                           f"{t.dtype} {tuple(t.shape)}")
+    if t.numel() and t.stride(2) != 1:
+        raise MixqError(1, f"the last dimension of {name} must be contiguous")
+    if t.device != cache.pages.device:
+        raise MixqError(1, f"{name} is on {t.device}, the cache on {cache.pages.device}")
+
+
+def _kv4_strides(t):
+    """(row, head) strides; those of a dimension of one say nothing and are set."""
+    head = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    return (t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1]) * head), head
+
+
+def _kv4_ints(cache: KV4Cache, name: str, t, shape):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or (t.numel() > 1 and t.stride(-1) != 1):
+        raise MixqError(1, f"{name} must be contiguous int32 {list(shape)}")
+    if t.device != cache.pages.device:
+        raise MixqError(1, f"{name} is on {t.device}, the cache on {cache.pages.device}")
+
+
+def _kv4_batch(cache: KV4Cache, table, per_seq, cu, rows: int):
+    """Checked (n_seqs, rows, table, width, stride) of a call's batch."""
+    if table.dim() != 2:
+        raise MixqError(1, "the block table must be int32 [n_seqs, width]")
+    n, width = table.shape
+    _kv4_ints(cache, "the block table", table, (n, width))
+    for name, t in per_seq:
+        _kv4_ints(cache, name, t, (n,))
+    if cu is not None:
+        _kv4_ints(cache, "the row offsets", cu, (n + 1,))
+    elif rows != n:
+        raise MixqError(1, f"without row offsets there must be one row per sequence, not {rows} "
+                           f"rows for {n} sequences")
+    return n, rows, table.data_ptr(), width, max(table.stride(0), width) if n > 1 else width
+
+
+class _On:
+    """The cache's device current, and `stream` (if given) the current stream, for a call."""
+
+    def __init__(self, cache: KV4Cache, stream):
+        import torch
+        if not cache.pages.is_cuda:
+            raise MixqError(6, "the cache must be on an sm_100 GPU")
+        self.todo = []
+        if cache.pages.device.index != torch.cuda.current_device():
+            self.todo.append(torch.cuda.device(cache.pages.device))
+        if stream is not None:
+            if stream.device != cache.pages.device:
+                raise MixqError(1, f"the stream is on {stream.device}, the cache on "
+                                   f"{cache.pages.device}")
+            self.todo.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.todo:
+            c.__enter__()
+
+    def __exit__(self, *e):
+        for c in reversed(self.todo):
+            c.__exit__(*e)
+
+
+def kv4_append(k, v, cache: KV4Cache, table, seq_lens, cu_new=None, status=None,
+               stream=None) -> None:
+    """Quantize new K and V rows [rows, n_kv_heads, head_dim] into the cache.
+
+    table int32 [n_seqs, width]: pages of each sequence; seq_lens int32 [n_seqs]: lengths with
+    the new rows; cu_new int32 [n_seqs + 1]: row offsets of the sequences (None: a row each).
+    Strides are free but for the last dimension (k and v may be parts of one projection)."""
+    _kv4_rows(cache, "k", k, cache.n_kv_heads)
+    _kv4_rows(cache, "v", v, cache.n_kv_heads)
+    if v.shape[0] != k.shape[0]:
+        raise MixqError(1, f"k has {k.shape[0]} rows, v {v.shape[0]}")
+    b = _kv4_batch(cache, table, (("seq_lens", seq_lens),), cu_new, k.shape[0])
+    with _On(cache, stream):
+        _check(lib().mixq_kv4_append(cache._ref, k.data_ptr(), *_kv4_strides(k), v.data_ptr(),
+                                     *_kv4_strides(v), *b,
+                                     seq_lens.data_ptr(), _ptr(cu_new), _ptr(status), _stream()))
+
+
+def kv4_read(cache: KV4Cache, table, cu_rows, rows: int, first=None, k_out=None, v_out=None,
+             status=None, stream=None):
+    """(K, V) rows [rows, n_kv_heads, head_dim] back from the cache.
+
+    Row cu_rows[s] + i is position first[s] + i of sequence s (first None: from 0; cu_rows None:
+    a row each); rows is the number of output rows."""
+    import torch
+    shape = (rows, cache.n_kv_heads, cache.head_dim)
+    b = _kv4_batch(cache, table, () if first is None else (("first", first),), cu_rows, rows)
+    with _On(cache, stream):
+        k_out = torch.empty(shape, dtype=cache.dtype, device=cache.pages.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=cache.dtype, device=cache.pages.device) if v_out is None else v_out
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            _kv4_rows(cache, name, t, cache.n_kv_heads)
+            if t.shape[0] != rows:
+                raise MixqError(1, f"{name} must have {rows} rows")
+        _check(lib().mixq_kv4_read(cache._ref, k_out.data_ptr(), *_kv4_strides(k_out),
+                                   v_out.data_ptr(), *_kv4_strides(v_out), *b, _ptr(first), _ptr(cu_rows), _ptr(status), _stream()))
+    return k_out, v_out
+
+
+_kv4_work_bytes: dict = {}  # (device index, head_dim) -> bytes
+
+
+def kv4_workspace(cache: KV4Cache):
+    """Scratch for kv4_attention (uint8; calls that may overlap on the GPU must not share one)."""
+    import torch
+    dev = cache.pages.device
+    n = _kv4_work_bytes.get((dev.index, cache.head_dim))
+    if n is None:
+        with torch.cuda.device(dev):
+            n = lib().mixq_kv4_attention_workspace_size(cache.head_dim, 0)
+        _kv4_work_bytes[dev.index, cache.head_dim] = n
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def kv4_attention(q, cache: KV4Cache, table, seq_lens, cu_new=None, max_new: int = 0, scale=None,
+                  window: int = 0, sinks: int = 0, out=None, work=None, status=None, stream=None):
+    """Causal attention of new tokens over the cache (which holds their K and V already).
+
+    q [rows, n_q_heads, head_dim]; table, seq_lens and cu_new as in kv4_append; max_new: a bound
+    on the new rows of one sequence, if known (a hint); scale: default head_dim ** -0.5;
+    window > 0: only the last `window` positions and the first `sinks` ones are seen; work:
+    scratch from kv4_workspace (default: allocated for the call).  Returns out [rows,
+    n_q_heads, head_dim]; a row that sees no key is zeros."""
+    import torch
+    _kv4_rows(cache, "q", q)
+    b = _kv4_batch(cache, table, (("seq_lens", seq_lens),), cu_new, q.shape[0])
+    with _On(cache, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _kv4_rows(cache, "out", out, q.shape[1])
+            if out.shape[0] != q.shape[0]:
+                raise MixqError(1, f"out must have {q.shape[0]} rows")
+        if work is None:
+            work = kv4_workspace(cache)
+        elif work.device != cache.pages.device or not work.is_contiguous():
+            raise MixqError(1, "work must be contiguous and on the cache's device")
+        n, rows, tptr, width, tstride = b
+        _check(lib().mixq_kv4_attention(
+            cache._ref, q.data_ptr(), *_kv4_strides(q), out.data_ptr(), *_kv4_strides(out), q.shape[1], n, rows, max_new, tptr, width, tstride,
+            seq_lens.data_ptr(), _ptr(cu_new),
+            cache.head_dim ** -0.5 if scale is None else float(scale), window, sinks,
+            work.data_ptr(), work.numel() * work.element_size(), _ptr(status), _stream()))
+    return out

@@ -12,6 +12,7 @@
 #include "../../include/mixq.h"
 #include "gemm_w4b.h"
 #include "internal.h"
+#include "kv4.h"
 
 namespace {
 
@@ -505,6 +506,164 @@ mixq_status mixq_debug_gemm_stall(int M, int N, int K, const int8_t *Xq, const v
   const char *why = nullptr;
   const cudaError_t e = mixq::launch_gemm(a, plan, static_cast<cudaStream_t>(stream), &why);
   return from_cuda(e, "stall gemm launch", why);
+}
+
+// ------------------------------------------------------------- 4-bit KV cache
+static bool kv4_dim(int d) { return d == 64 || d == 128; }
+
+size_t mixq_kv4_page_bytes(int page_size, int head_dim) {
+  if (page_size <= 0 || page_size % 16 || !kv4_dim(head_dim)) return 0;
+  return static_cast<size_t>(page_size) * (head_dim + 8);
+}
+
+static mixq_status kv4_check(const mixq_kv4_cache *c, int n_seqs, int n_rows, const int32_t *table,
+                             int table_width, int64_t table_stride, const int32_t *cu,
+                             mixq::Kv4Cache *cache, mixq::Kv4Batch *b) {
+  if (!c) return fail(MIXQ_ERR_INVALID_ARG, "cache must be non-null");
+  if (c->dtype != MIXQ_KV4_F16 && c->dtype != MIXQ_KV4_BF16)
+    return fail(MIXQ_ERR_INVALID_ARG, "cache dtype = %d must be MIXQ_KV4_F16 or MIXQ_KV4_BF16",
+                c->dtype);
+  if (!kv4_dim(c->head_dim))
+    return fail(MIXQ_ERR_UNSUPPORTED_SHAPE, "head_dim = %d must be 64 or 128", c->head_dim);
+  if (c->page_size <= 0 || c->page_size % 16)
+    return fail(MIXQ_ERR_UNSUPPORTED_SHAPE, "page_size = %d must be a positive multiple of 16",
+                c->page_size);
+  if (c->n_kv_heads <= 0 || c->n_kv_heads > 65535 || c->n_pages < 0)
+    return fail(MIXQ_ERR_UNSUPPORTED_SHAPE, "n_kv_heads = %d must lie in [1, 65535], n_pages = %d be >= 0",
+                c->n_kv_heads, c->n_pages);
+  const int64_t page = static_cast<int64_t>(c->n_kv_heads) *
+                       static_cast<int64_t>(mixq_kv4_page_bytes(c->page_size, c->head_dim));
+  if (c->page_stride < page || c->page_stride % 16)
+    return fail(MIXQ_ERR_INVALID_ARG, "page_stride = %lld must be a multiple of 16 and >= %lld",
+                static_cast<long long>(c->page_stride), static_cast<long long>(page));
+  if (n_seqs < 0 || n_rows < 0 || n_seqs > (1 << 28) || n_rows > (1 << 30))
+    return fail(MIXQ_ERR_UNSUPPORTED_SHAPE, "n_seqs = %d or n_rows = %d out of range", n_seqs, n_rows);
+  if (!cu && n_rows != n_seqs)
+    return fail(MIXQ_ERR_INVALID_ARG, "without cu, n_rows = %d must equal n_seqs = %d", n_rows, n_seqs);
+  if (table_width < 0 || table_stride < table_width)
+    return fail(MIXQ_ERR_INVALID_ARG, "table_width = %d must be >= 0 and table_stride >= table_width",
+                table_width);
+  if (n_seqs > 0 && table_width > 0 && !table)
+    return fail(MIXQ_ERR_INVALID_ARG, "table must be non-null");
+  if (c->n_pages > 0 && !c->pages) return fail(MIXQ_ERR_INVALID_ARG, "pages must be non-null");
+  if (!aligned16(c->pages)) return fail(MIXQ_ERR_MISALIGNED, "pages must be 16-byte aligned");
+  *cache = mixq::Kv4Cache{static_cast<uint8_t *>(c->pages), c->page_stride, c->n_pages,
+                          c->page_size / 16, c->n_kv_heads, c->head_dim,
+                          c->dtype == MIXQ_KV4_BF16};
+  *b = mixq::Kv4Batch{n_seqs, table, table_width, table_stride, nullptr, cu, n_rows};
+  return MIXQ_OK;
+}
+
+static mixq_status kv4_check_rows(const char *name, const void *p, int64_t row, int64_t head,
+                                  bool written, int heads, int d) {
+  if (!p) return fail(MIXQ_ERR_INVALID_ARG, "%s must be non-null", name);
+  if (!aligned16(p)) return fail(MIXQ_ERR_MISALIGNED, "%s must be 16-byte aligned", name);
+  if (row < 0 || head < 0 || row % 8 || head % 8)
+    return fail(MIXQ_ERR_INVALID_ARG, "strides of %s must be multiples of 8 and >= 0", name);
+  if (written && (row < d || (heads > 1 && head < d)))
+    return fail(MIXQ_ERR_INVALID_ARG, "rows of %s overlap", name);
+  return MIXQ_OK;
+}
+
+mixq_status mixq_kv4_append(const mixq_kv4_cache *cache, const void *k, int64_t k_row,
+                            int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
+                            int n_seqs, int n_rows, const int32_t *table, int table_width,
+                            int64_t table_stride, const int32_t *seq_lens, const int32_t *cu,
+                            int32_t *status, void *stream) {
+  mixq::Kv4Cache c;
+  mixq::Kv4Batch b;
+  mixq_status s = kv4_check(cache, n_seqs, n_rows, table, table_width, table_stride, cu, &c, &b);
+  if (s != MIXQ_OK) return s;
+  if (n_rows == 0 || n_seqs == 0) return ok();
+  if (!seq_lens) return fail(MIXQ_ERR_INVALID_ARG, "seq_lens must be non-null");
+  if ((s = kv4_check_rows("k", k, k_row, k_head, false, c.n_kv, c.d)) != MIXQ_OK) return s;
+  if ((s = kv4_check_rows("v", v, v_row, v_head, false, c.n_kv, c.d)) != MIXQ_OK) return s;
+  if ((s = check_device(nullptr)) != MIXQ_OK) return s;
+  b.lens = seq_lens;
+  return from_cuda(mixq::launch_kv4_append(c, b, mixq::Kv4Rows{k, v, k_row, k_head, v_row, v_head},
+                                           status, static_cast<cudaStream_t>(stream)),
+                   "KV4 append launch");
+}
+
+mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_row,
+                          int64_t k_head, void *v_out, int64_t v_row, int64_t v_head,
+                          int n_seqs, int n_rows, const int32_t *table, int table_width,
+                          int64_t table_stride, const int32_t *first, const int32_t *cu,
+                          int32_t *status, void *stream) {
+  mixq::Kv4Cache c;
+  mixq::Kv4Batch b;
+  mixq_status s = kv4_check(cache, n_seqs, n_rows, table, table_width, table_stride, cu, &c, &b);
+  if (s != MIXQ_OK) return s;
+  if (n_rows == 0 || n_seqs == 0) return ok();
+  if ((s = kv4_check_rows("k_out", k_out, k_row, k_head, true, c.n_kv, c.d)) != MIXQ_OK) return s;
+  if ((s = kv4_check_rows("v_out", v_out, v_row, v_head, true, c.n_kv, c.d)) != MIXQ_OK) return s;
+  if ((s = check_device(nullptr)) != MIXQ_OK) return s;
+  b.lens = first;
+  return from_cuda(mixq::launch_kv4_read(c, b, mixq::Kv4Rows{k_out, v_out, k_row, k_head, v_row, v_head},
+                                         status, static_cast<cudaStream_t>(stream)),
+                   "KV4 read launch");
+}
+
+size_t mixq_kv4_attention_workspace_size(int head_dim, int num_sms) {
+  if (!kv4_dim(head_dim)) return 0;
+  if (num_sms <= 0) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    num_sms = mixq::device_sm_count(dev);
+  }
+  return num_sms > 0 ? mixq::kv4_attn_workspace(head_dim, num_sms) : 0;
+}
+
+mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64_t q_row,
+                               int64_t q_head, void *out, int64_t o_row, int64_t o_head,
+                               int n_q_heads, int n_seqs, int n_rows, int max_new,
+                               const int32_t *table, int table_width, int64_t table_stride,
+                               const int32_t *seq_lens, const int32_t *cu, float scale,
+                               int window, int sinks, void *work, size_t work_bytes,
+                               int32_t *status, void *stream) {
+  mixq::Kv4AttnArgs a{};
+  mixq_status s = kv4_check(cache, n_seqs, n_rows, table, table_width, table_stride, cu, &a.c, &a.b);
+  if (s != MIXQ_OK) return s;
+  if (n_q_heads <= 0 || n_q_heads % a.c.n_kv)
+    return fail(MIXQ_ERR_UNSUPPORTED_SHAPE, "n_q_heads = %d must be a positive multiple of n_kv_heads = %d",
+                n_q_heads, a.c.n_kv);
+  if (!(scale - scale == 0.f)) return fail(MIXQ_ERR_INVALID_ARG, "scale must be finite");
+  if (window < 0 || sinks < 0 || max_new < 0)
+    return fail(MIXQ_ERR_INVALID_ARG, "window, sinks and max_new must be >= 0");
+  if (static_cast<int64_t>(n_rows) * (n_q_heads / a.c.n_kv) > (1ll << 30))
+    return fail(MIXQ_ERR_UNSUPPORTED_SHAPE, "too many query rows");
+  if (n_rows == 0 || n_seqs == 0) return ok();
+  if (!seq_lens) return fail(MIXQ_ERR_INVALID_ARG, "seq_lens must be non-null");
+  if ((s = kv4_check_rows("q", q, q_row, q_head, false, n_q_heads, a.c.d)) != MIXQ_OK) return s;
+  if ((s = kv4_check_rows("out", out, o_row, o_head, true, n_q_heads, a.c.d)) != MIXQ_OK) return s;
+  if (out == q) return fail(MIXQ_ERR_INVALID_ARG, "out must not overlap q");
+  if (!work) return fail(MIXQ_ERR_INVALID_ARG, "work must be non-null");
+  if (!aligned16(work)) return fail(MIXQ_ERR_MISALIGNED, "work must be 16-byte aligned");
+  if ((s = check_device(&a.num_sms)) != MIXQ_OK) return s;
+  if (work_bytes < mixq::kv4_attn_workspace(a.c.d, a.num_sms))
+    return fail(MIXQ_ERR_INVALID_ARG, "work_bytes = %zu must be at least %zu", work_bytes,
+                mixq::kv4_attn_workspace(a.c.d, a.num_sms));
+  a.b.lens = seq_lens;
+  a.q = q;
+  a.out = out;
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.o_row = o_row;
+  a.o_head = o_head;
+  a.n_q = n_q_heads;
+  a.group = n_q_heads / a.c.n_kv;
+  a.max_new = !cu ? 1 : max_new > 0 && max_new < n_rows ? max_new : n_rows;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.work = static_cast<float *>(work);
+  a.status = status;
+  const char *why = nullptr;
+  const cudaError_t e = mixq::launch_kv4_attn(a, static_cast<cudaStream_t>(stream), &why);
+  return from_cuda(e, "KV4 attention launch", why);
 }
 
 mixq_status mixq_debug_mma_rate(int kind, int iters, double *ops, int32_t *status, void *stream) {

@@ -1,0 +1,328 @@
+// Append and read of the 4-bit KV cache (QServe W4A8KV4 notes: each token and
+// head of K and V is its own 4-bit asymmetric group).
+//
+//   append: lo = min x, hi = max x, s = T((hi - lo) / 15),
+//           c = min(rint((x - lo) * (1 / s)), 15)           (fp32, each step rounded once)
+//   read:   x^ = c * s + lo                                  (fp32, rounded once to T)
+//
+// Both passes are bound by HBM: 4*D bytes of rows against D + 8 bytes of cache
+// per token and kv head.  A warp owns one 16-token record of one kv head.  A
+// row of D values is held by D/8 lanes, 16 bytes each, so rows move in whole
+// 128- or 256-byte segments, a row's range takes log2(D/8) shuffles, and K's
+// eight 4-bit codes of a lane are exactly one word of the record.  The V words
+// of a record hold four tokens (2t, 2t+8, 2t+1, 2t+9), which one group of D/8
+// lanes loads as four rows; a 4x4 byte transpose in registers turns their codes
+// into whole words.
+#include <cuda_runtime.h>
+
+#include "kv4.h"
+#include "ptx.cuh"
+
+namespace mixq {
+namespace {
+
+constexpr int kWarps = 8;
+
+// First sequence of the virtual record index v.  Sequence s owns the indexes
+// from floor(cu[s] / 16) + 2 s: at least one more than the records its rows can
+// touch, so every record has an index and the search needs cu alone.
+__device__ __forceinline__ int find_seq(const Kv4Batch &b, int v, int lane) {
+  int lo = 0, hi = b.n_seqs - 1;  // answer in [lo, hi]: last s with start(s) <= v
+  while (lo < hi) {
+    // 32 probes split the range: last probe whose start is <= v
+    const int n = hi - lo;
+    const int step = (n + 31) / 32;
+    const int s = min(lo + (lane + 1) * step, hi);
+    const int start = (__ldg(b.cu + s) >> 4) + 2 * s;
+    const unsigned m = __ballot_sync(0xffffffffu, start <= v);
+    const int k = __popc(m);  // starts do not fall, so m is a prefix of the lanes
+    const int nlo = k == 0 ? lo : min(lo + k * step, hi);
+    hi = k == 32 ? hi : min(lo + (k + 1) * step - 1, hi);
+    lo = nlo;
+    hi = max(hi, lo);
+  }
+  return lo;
+}
+
+struct Place {
+  int row0;       // row of the record's token 0 (may lie before the range)
+  int t0, t1;     // tokens [t0, t1) of the record belong to the call
+  uint8_t *rec;   // record of kv head 0
+};
+
+// The record that virtual index v stands for, or t0 == t1.
+__device__ __forceinline__ Place locate(const Kv4Cache &c, const Kv4Batch &b, int v, int lane,
+                                        bool append, int32_t *status) {
+  Place p{0, 0, 0, nullptr};
+  int s, local;
+  if (b.cu) {
+    s = find_seq(b, v, lane);
+    local = v - ((__ldg(b.cu + s) >> 4) + 2 * s);
+  } else {
+    s = v;
+    local = 0;
+  }
+  bool bad = false;
+  const int2 r = kv4_row_range(b, s, &bad);
+  const int n = r.y - r.x;
+  if (bad && lane == 0) record_error(status, kErrInvalidArg);
+  if (n == 0) return p;
+  // positions [first, first + n)
+  const int first = append ? __ldg(b.lens + s) - n : (b.lens ? __ldg(b.lens + s) : 0);
+  const int from = max(first, 0);
+  if (first + static_cast<int64_t>(n) <= from) return p;
+  const int rec = (from >> 4) + local;
+  const int64_t base = static_cast<int64_t>(rec) * 16;
+  const int64_t t0 = max(static_cast<int64_t>(from) - base, static_cast<int64_t>(0));
+  const int64_t t1 = min(first + static_cast<int64_t>(n) - base, static_cast<int64_t>(16));
+  if (t1 <= t0) return p;
+  const int slot = rec / c.recs_per_page;
+  const int page = slot < b.table_width ? __ldg(b.table + s * b.table_stride + slot) : -1;
+  if (page < 0 || page >= c.n_pages) {
+    if (lane == 0) record_error(status, kErrInvalidArg);
+    return p;
+  }
+  p.t0 = static_cast<int>(t0);
+  p.t1 = static_cast<int>(t1);
+  p.row0 = static_cast<int>(r.x + (base - first));
+  p.rec = c.pages + page * c.page_stride +
+          static_cast<int64_t>(rec - slot * c.recs_per_page) * kv4_rec_bytes(c.d);
+  return p;
+}
+
+// Transpose of a 4x4 byte matrix held as four words.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+  const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+  w[0] = __byte_perm(a, b, 0x5410);
+  w[1] = __byte_perm(a, b, 0x7632);
+  w[2] = __byte_perm(c, d, 0x5410);
+  w[3] = __byte_perm(c, d, 0x7632);
+}
+
+// Token that byte i of a V word of quad t belongs to.
+__device__ __forceinline__ int quad_token(int t, int i) { return 2 * t + (i >> 1) + 8 * (i & 1); }
+
+// The eight codes of a lane (one row spread over LANES lanes) as nibbles
+// 0..7 = elements 0..7, and the row's (s, lo) pair.
+template <typename T, int LANES>
+__device__ __forceinline__ uint32_t quantize8(const uint4 &raw, uint32_t *pair) {
+  using X = Kv4Type<T>;
+  using T2 = typename X::T2;
+  const T2 x[4] = {kv4_bits<T2>(raw.x), kv4_bits<T2>(raw.y), kv4_bits<T2>(raw.z),
+                   kv4_bits<T2>(raw.w)};
+  // the *_nan forms keep a NaN, so a row with one ends as (NaN, NaN)
+  T2 mn = __hmin2_nan(__hmin2_nan(x[0], x[1]), __hmin2_nan(x[2], x[3]));
+  T2 mx = __hmax2_nan(__hmax2_nan(x[0], x[1]), __hmax2_nan(x[2], x[3]));
+  // (min x, min -x) in one register: one shuffle per step serves both ends
+  const uint32_t a = kv4_bits<uint32_t>(mn), z = kv4_bits<uint32_t>(mx);
+  T2 e = __hmin2_nan(kv4_bits<T2>(__byte_perm(a, z, 0x5410) ^ 0x80000000u),
+                     kv4_bits<T2>(__byte_perm(a, z, 0x7632) ^ 0x80000000u));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1)
+    e = __hmin2_nan(e, kv4_bits<T2>(__shfl_xor_sync(0xffffffffu, kv4_bits<uint32_t>(e), o)));
+  const float2 ends = X::f2(e);
+  const float lo = ends.x, hi = -ends.y;
+  const float range = __fsub_rn(hi, lo);
+  const T2 sl = X::from2(__fdiv_rn(range, 15.f), lo);
+  float s = X::f2(sl).x;
+  if (s < 1.17549435e-38f) s = 0.f;  // a bf16 subnormal's reciprocal may not be finite
+  const bool finite = range - range == 0.f;  // neither end NaN or infinite, nor their distance
+  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = X::f2(x[i]);
+    const float u = fminf(__fmul_rn(__fsub_rn(f.x, lo), inv), 15.f);
+    const float w = fminf(__fmul_rn(__fsub_rn(f.y, lo), inv), 15.f);
+    // 1.5 * 2^23 + u: round half to even, code in the low bits
+    codes |= (__float_as_uint(__fadd_rn(u, 12582912.f)) & 15u) << (8 * i);
+    codes |= (__float_as_uint(__fadd_rn(w, 12582912.f)) & 15u) << (8 * i + 4);
+  }
+  *pair = finite ? kv4_bits<uint32_t>(X::from2(s, lo)) : 0x7fff7fffu;
+  return codes;
+}
+
+// Nibbles 0..7 = dims 0..7 -> K word (nibble p = dim 2p, nibble p + 4 = dim 2p + 1).
+__device__ __forceinline__ uint32_t k_word(uint32_t c) {
+  uint32_t even = c & 0x0f0f0f0fu, odd = (c >> 4) & 0x0f0f0f0fu;
+  even = (even | (even >> 4)) & 0x00ff00ffu;
+  odd = (odd | (odd >> 4)) & 0x00ff00ffu;
+  return __byte_perm(even, odd, 0x6420);
+}
+
+__device__ __forceinline__ uint32_t k_unword(uint32_t w) {
+  uint32_t even = __byte_perm(w, 0, 0x4140), odd = __byte_perm(w, 0, 0x4342);
+  even = (even | (even << 4)) & 0x0f0f0f0fu;
+  odd = (odd | (odd << 4)) & 0x0f0f0f0fu;
+  return even | (odd << 4);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+    kv4_append_kernel(Kv4Cache c, Kv4Batch b, Kv4Rows r, int32_t *status) {
+  constexpr int LANES = D / 8, RPW = 32 / LANES;  // lanes per row, rows per warp load
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * kWarps + warp;
+  if (h >= c.n_kv) return;
+  const Place p = locate(c, b, blockIdx.x, lane, true, status);
+  if (p.t0 >= p.t1) return;
+  const int sub = lane / LANES, l = lane % LANES;
+  uint8_t *rec = p.rec + h * static_cast<int64_t>(c.recs_per_page) * kv4_rec_bytes(D);
+  const T *k = static_cast<const T *>(r.k) + h * r.k_head + l * 8;
+  const T *v = static_cast<const T *>(r.v) + h * r.v_head + l * 8;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+
+  // Rows come in V's quad order for both K and V: one lane group loads the four
+  // tokens of a quad.  All loads of a half record are issued before their use.
+#pragma unroll
+  for (int it = 0; it < 4 / RPW; ++it) {
+    const int t = it * RPW + sub;
+    uint4 kr[4], vr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = quad_token(t, i);
+      const bool in = tok >= p.t0 && tok < p.t1;
+      const int64_t row = p.row0 + tok;
+      kr[i] = in ? __ldg(reinterpret_cast<const uint4 *>(k + row * r.k_row)) : zero;
+      vr[i] = in ? __ldg(reinterpret_cast<const uint4 *>(v + row * r.v_row)) : zero;
+    }
+    uint32_t vw[4];
+    int valid = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = quad_token(t, i);
+      const bool in = tok >= p.t0 && tok < p.t1;
+      uint32_t kp, vp;
+      const uint32_t kc = quantize8<T, LANES>(kr[i], &kp);
+      vw[i] = quantize8<T, LANES>(vr[i], &vp);
+      if (in) {
+        valid |= 1 << i;
+        reinterpret_cast<uint32_t *>(rec + tok * (D / 2))[l] = k_word(kc);
+        if (l == 0) {
+          reinterpret_cast<uint32_t *>(rec + 16 * D)[tok] = kp;
+          reinterpret_cast<uint32_t *>(rec + 16 * D + 64)[tok] = vp;
+        }
+      }
+    }
+    transpose4(vw);  // word j: byte column 4 l + j, byte i = token i of the quad
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint8_t *w = rec + 8 * D + (l >> 3) * 512 + (4 * (l & 1) + j) * 64 + t * 16 + ((l >> 1) & 3) * 4;
+      if (valid == 15) {
+        *reinterpret_cast<uint32_t *>(w) = vw[j];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (valid >> i & 1) w[i] = static_cast<uint8_t>(vw[j] >> (8 * i));
+      }
+    }
+  }
+}
+
+// Eight codes (nibbles 0..7) and the row's pair -> eight values of T.
+template <typename T>
+__device__ __forceinline__ uint4 dequantize8(uint32_t c, float2 sl) {
+  using X = Kv4Type<T>;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // 2^23 + code as bits, exact; c * s is exact, so the sum rounds once
+    const float a = __uint_as_float(0x4b000000u | ((c >> (8 * i)) & 15u)) - 8388608.f;
+    const float b = __uint_as_float(0x4b000000u | ((c >> (8 * i + 4)) & 15u)) - 8388608.f;
+    float x = fmaf(a, sl.x, sl.y), y = fmaf(b, sl.x, sl.y);
+    // s was rounded, so 15 s + lo can pass the type's largest value: hold it there (NaN passes)
+    x = x > X::max_finite ? X::max_finite : x;
+    y = y > X::max_finite ? X::max_finite : y;
+    o[i] = kv4_bits<uint32_t>(X::from2(x, y));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+    kv4_read_kernel(Kv4Cache c, Kv4Batch b, Kv4Rows r, int32_t *status) {
+  constexpr int LANES = D / 8, RPW = 32 / LANES;
+  constexpr bool BF = Kv4Type<T>::bf16;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * kWarps + warp;
+  if (h >= c.n_kv) return;
+  const Place p = locate(c, b, blockIdx.x, lane, false, status);
+  if (p.t0 >= p.t1) return;
+  const int sub = lane / LANES, l = lane % LANES;
+  const uint8_t *rec = p.rec + h * static_cast<int64_t>(c.recs_per_page) * kv4_rec_bytes(D);
+  T *k = const_cast<T *>(static_cast<const T *>(r.k)) + h * r.k_head + l * 8;
+  T *v = const_cast<T *>(static_cast<const T *>(r.v)) + h * r.v_head + l * 8;
+  uint32_t kw[4 / RPW][4], vw[4 / RPW][4], kp[4 / RPW][4], vp[4 / RPW][4];
+#pragma unroll
+  for (int it = 0; it < 4 / RPW; ++it) {
+    const int t = it * RPW + sub;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = quad_token(t, i);
+      kw[it][i] = reinterpret_cast<const uint32_t *>(rec + tok * (D / 2))[l];
+      vw[it][i] = *reinterpret_cast<const uint32_t *>(rec + 8 * D + (l >> 3) * 512 +
+                                                      (4 * (l & 1) + i) * 64 + t * 16 + ((l >> 1) & 3) * 4);
+      kp[it][i] = reinterpret_cast<const uint32_t *>(rec + 16 * D)[tok];
+      vp[it][i] = reinterpret_cast<const uint32_t *>(rec + 16 * D + 64)[tok];
+    }
+  }
+#pragma unroll
+  for (int it = 0; it < 4 / RPW; ++it) {
+    const int t = it * RPW + sub;
+    transpose4(vw[it]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = quad_token(t, i);
+      if (tok < p.t0 || tok >= p.t1) continue;
+      const int64_t row = p.row0 + tok;
+      *reinterpret_cast<uint4 *>(k + row * r.k_row) =
+          dequantize8<T>(k_unword(kw[it][i]), kv4_pair<BF>(kp[it][i]));
+      *reinterpret_cast<uint4 *>(v + row * r.v_row) =
+          dequantize8<T>(vw[it][i], kv4_pair<BF>(vp[it][i]));
+    }
+  }
+}
+
+template <typename K>
+cudaError_t launch(K kernel, const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows &r,
+                   int32_t *status, cudaStream_t stream) {
+  // virtual records: one per sequence, or the last start plus the last sequence's own
+  const int64_t n = b.cu ? static_cast<int64_t>(b.rows / 16) + 2ll * b.n_seqs : b.n_seqs;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(n), (c.n_kv + kWarps - 1) / kWarps, 1);
+  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, c, b, r, status);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows &r,
+                              int32_t *status, cudaStream_t stream) {
+  if (c.bf16)
+    return c.d == 128 ? launch(kv4_append_kernel<__nv_bfloat16, 128>, c, b, r, status, stream)
+                      : launch(kv4_append_kernel<__nv_bfloat16, 64>, c, b, r, status, stream);
+  return c.d == 128 ? launch(kv4_append_kernel<__half, 128>, c, b, r, status, stream)
+                    : launch(kv4_append_kernel<__half, 64>, c, b, r, status, stream);
+}
+
+cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows &r,
+                            int32_t *status, cudaStream_t stream) {
+  if (c.bf16)
+    return c.d == 128 ? launch(kv4_read_kernel<__nv_bfloat16, 128>, c, b, r, status, stream)
+                      : launch(kv4_read_kernel<__nv_bfloat16, 64>, c, b, r, status, stream);
+  return c.d == 128 ? launch(kv4_read_kernel<__half, 128>, c, b, r, status, stream)
+                    : launch(kv4_read_kernel<__half, 64>, c, b, r, status, stream);
+}
+
+}  // namespace mixq

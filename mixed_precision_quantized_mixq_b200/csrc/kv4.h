@@ -1,0 +1,120 @@
+// The 4-bit KV cache: page format constants, the launch arguments of its
+// kernels (kv4.cu: append and read; kv4_attn.cu: attention) and the device
+// helpers they share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mixq {
+
+// Tokens per record.  A record is [16][D/2] K bytes, the interleaved V bytes
+// (16*D/2) and one 4-byte (s, lo) pair per token for K, then for V.
+constexpr int kKv4Rec = 16;
+__host__ __device__ constexpr int kv4_rec_bytes(int d) { return kKv4Rec * (d + 8); }
+
+struct Kv4Cache {
+  uint8_t *pages;
+  int64_t page_stride;  // bytes between pages
+  int n_pages;
+  int recs_per_page;
+  int n_kv;
+  int d;     // 64 or 128
+  int bf16;  // type of the rows and of the (s, lo) pairs
+};
+
+struct Kv4Batch {
+  int n_seqs;
+  const int32_t *table;  // [n_seqs][table_width]
+  int table_width;
+  int64_t table_stride;
+  const int32_t *lens;  // append, attention: tokens stored after the call; read: first position (or null)
+  const int32_t *cu;    // [n_seqs + 1] row offsets, null: one row per sequence
+  int rows;             // rows in the row tensors
+};
+
+struct Kv4Rows {  // K and V rows [rows][n_kv][d]; strides in elements
+  const void *k, *v;
+  int64_t k_row, k_head, v_row, v_head;
+};
+
+struct Kv4AttnArgs {
+  Kv4Cache c;
+  Kv4Batch b;
+  const void *q;
+  void *out;
+  int64_t q_row, q_head, o_row, o_head;
+  int n_q;    // query heads
+  int group;  // n_q / n_kv
+  int max_new;
+  float scale;
+  int window, sinks;  // window 0: all keys up to the query's position
+  float *work;
+  int num_sms;
+  int32_t *status;
+};
+
+cudaError_t launch_kv4_append(const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows &r,
+                              int32_t *status, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows &r,
+                            int32_t *status, cudaStream_t stream);
+size_t kv4_attn_workspace(int d, int num_sms);
+cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream, const char **why);
+
+#ifdef __CUDACC__
+
+// Row range of sequence s in the row tensors; a range that is not ordered or
+// leaves the tensor counts as empty.  bad: such a range was seen.
+__device__ __forceinline__ int2 kv4_row_range(const Kv4Batch &b, int s, bool *bad) {
+  if (!b.cu) return make_int2(s, s + 1);
+  const int r0 = __ldg(b.cu + s), r1 = __ldg(b.cu + s + 1);
+  if (r0 < 0 || r1 < r0 || r1 > b.rows) {
+    *bad = true;
+    return make_int2(0, 0);
+  }
+  return make_int2(r0, r1);
+}
+
+// An (s, lo) pair as two fp32 values.
+template <bool BF16>
+__device__ __forceinline__ float2 kv4_pair(uint32_t p) {
+  if (BF16) return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+  __half2 h;
+  memcpy(&h, &p, 4);
+  return __half22float2(h);
+}
+
+template <typename T>
+struct Kv4Type;
+template <>
+struct Kv4Type<__half> {
+  using T2 = __half2;
+  static constexpr bool bf16 = false;
+  static __device__ __forceinline__ float2 f2(__half2 v) { return __half22float2(v); }
+  static __device__ __forceinline__ __half2 from2(float a, float b) { return __floats2half2_rn(a, b); }
+  static constexpr float max_finite = 65504.f;
+};
+template <>
+struct Kv4Type<__nv_bfloat16> {
+  using T2 = __nv_bfloat162;
+  static constexpr bool bf16 = true;
+  static __device__ __forceinline__ float2 f2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+  static __device__ __forceinline__ __nv_bfloat162 from2(float a, float b) {
+    return __floats2bfloat162_rn(a, b);
+  }
+  static constexpr float max_finite = 3.3895313892515355e38f;
+};
+
+template <typename A, typename B>
+__device__ __forceinline__ A kv4_bits(B b) {
+  static_assert(sizeof(A) == sizeof(B), "same size");
+  A a;
+  memcpy(&a, &b, sizeof a);
+  return a;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace mixq
