@@ -404,10 +404,12 @@ mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_ro
  * query head h reads kv head h / (n_q_heads / n_kv_heads):
  *   key j is visible when j <= p and (window == 0 or j > p - window or j < sinks)
  *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * (q . k_j) - max)
- * over the visible keys, k_j and v_j the rows c * s + lo unrounded, scores, sums
- * and products in fp32, weights times V's scale in fp16 under a power of two.  A
- * row that sees no key is written as zeros.  The codes enter the products as they
- * are; a NaN in a row reaches only those queries that see the row.
+ * over the visible keys; scores from K's codes and pairs as they are, scores, sums
+ * and accumulation in fp32.  Sequences with at most 32 rows (new tokens times
+ * grouped heads) per kv head take V's codes and pairs as they are too, weights
+ * times V's scale in fp16 under a power of two; with more rows the weights and V's
+ * rows are rounded to T for their product.  A row that sees no key is written as
+ * zeros; a NaN in a row reaches only those queries that see the row.
  *   q, out   [n_rows][n_q_heads][head_dim], strides in elements, multiples of 8;
  *            16-byte aligned; out must not overlap q
  *   max_new  a bound on cu[s+1] - cu[s], or 0 for none: it picks the kernel, the

@@ -655,15 +655,13 @@ mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64
   a.o_head = o_head;
   a.n_q = n_q_heads;
   a.group = n_q_heads / a.c.n_kv;
-  a.max_new = !cu ? 1 : max_new > 0 && max_new < n_rows ? max_new : n_rows;
+  a.max_rows = static_cast<int64_t>(!cu ? 1 : max_new > 0 && max_new < n_rows ? max_new : n_rows) * a.group;
   a.scale = scale;
   a.window = window;
   a.sinks = sinks;
   a.work = static_cast<float *>(work);
   a.status = status;
-  const char *why = nullptr;
-  const cudaError_t e = mixq::launch_kv4_attn(a, static_cast<cudaStream_t>(stream), &why);
-  return from_cuda(e, "KV4 attention launch", why);
+  return from_cuda(mixq::launch_kv4_attn(a, static_cast<cudaStream_t>(stream)), "KV4 attention launch");
 }
 
 mixq_status mixq_debug_mma_rate(int kind, int iters, double *ops, int32_t *status, void *stream) {

@@ -48,7 +48,8 @@ struct Kv4AttnArgs {
   int64_t q_row, q_head, o_row, o_head;
   int n_q;    // query heads
   int group;  // n_q / n_kv
-  int max_new;
+  int64_t max_rows;    // bound on a sequence's rows of a kv head (new tokens x group)
+  int64_t tile_above;  // sequences with more rows than this belong to the tile kernel
   float scale;
   int window, sinks;  // window 0: all keys up to the query's position
   float *work;
@@ -61,7 +62,10 @@ cudaError_t launch_kv4_append(const Kv4Cache &c, const Kv4Batch &b, const Kv4Row
 cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows &r,
                             int32_t *status, cudaStream_t stream);
 size_t kv4_attn_workspace(int d, int num_sms);
-cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream, const char **why);
+// Decode steps and small row counts (kv4_attn.cu), many rows (kv4_tile.cu); the
+// first launches the second where it is needed.
+cudaError_t launch_kv4_attn(Kv4AttnArgs a, cudaStream_t stream);
+cudaError_t launch_kv4_tile(const Kv4AttnArgs &a, cudaStream_t stream);
 
 #ifdef __CUDACC__
 

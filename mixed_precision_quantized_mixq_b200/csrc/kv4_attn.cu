@@ -38,6 +38,7 @@ constexpr float kNegBig = -1e30f;  // running maximum before the first visible k
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMinQuota = 16;  // records: below two a warp, a cut costs more than it spreads
 constexpr int kMaxRows = 16;
+constexpr int kTileAbove = 32;
 
 struct Desc {  // item whose last part is not in the CTA that starts it
   int seq, item, last, pad;
@@ -69,7 +70,8 @@ __device__ __forceinline__ Seq load_seq(const Kv4AttnArgs &a, int s) {
     if (threadIdx.x == 0) record_error(a.status, kErrInvalidArg);
   }
   q.pos0 = full - q.nq;
-  q.tiles = static_cast<int>((static_cast<int64_t>(q.nq) * a.group + R - 1) / R);
+  const int64_t rows = static_cast<int64_t>(q.nq) * a.group;
+  q.tiles = rows > a.tile_above ? 0 : static_cast<int>((rows + R - 1) / R);
   const int total = (q.len + kKv4Rec - 1) / kKv4Rec;
   q.skip_at = total;
   q.skip_by = 0;
@@ -690,8 +692,7 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
 template <typename T, int D>
 cudaError_t pick(const Kv4AttnArgs &a, cudaStream_t stream) {
   // 8 rows per tile while a sequence's rows of a kv head fit one such tile
-  const int64_t rows = static_cast<int64_t>(a.max_new) * a.group;
-  return rows <= 8 ? launch<T, D, 1>(a, stream) : launch<T, D, 2>(a, stream);
+  return a.max_rows <= 8 ? launch<T, D, 1>(a, stream) : launch<T, D, 2>(a, stream);
 }
 
 }  // namespace
@@ -701,8 +702,16 @@ size_t kv4_attn_workspace(int d, int num_sms) {
   return ctas * sizeof(Desc) + ctas * 2 * slot_floats(d) * sizeof(float);
 }
 
-cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, cudaStream_t stream, const char **why) {
-  (void)why;
+cudaError_t launch_kv4_attn(Kv4AttnArgs a, cudaStream_t stream) {
+  // A sequence with more than kTileAbove rows per kv head goes to the tile kernel; the lengths are
+  // on the device, so a call whose bound allows both kinds launches both, and each skips the other's.
+  a.tile_above = INT64_MAX;
+  if (a.max_rows > kTileAbove) {
+    a.tile_above = kTileAbove;
+    const cudaError_t e = launch_kv4_tile(a, stream);
+    if (e != cudaSuccess) return e;
+    a.max_rows = kTileAbove;
+  }
   if (a.c.bf16)
     return a.c.d == 128 ? pick<__nv_bfloat16, 128>(a, stream) : pick<__nv_bfloat16, 64>(a, stream);
   return a.c.d == 128 ? pick<__half, 128>(a, stream) : pick<__half, 64>(a, stream);

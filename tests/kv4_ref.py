@@ -117,7 +117,10 @@ def attention(pages: Pages, q, table, lens, cu, scale, window=0, sinks=0):
         relative, numerator and denominator together;
       the exponential (2^-22 relative, and 2^-23 of its argument's magnitude) and fp32 sums of n
         terms spread over lanes, warps and parts: 2^-17 (1 + n / 2048) of A + B covers both, with
-        B = sum p |lo| / sum p."""
+        B = sum p |lo| / sum p;
+      where a sequence has more than 32 rows per kv head, the tile kernel's operands: weights and V
+        rows rounded once each to the type, so every term p v is off by at most 2 (eps/2) |p v|:
+        eps C with C = sum p |v| / sum p (second-order terms are below the fp32 allowance above)."""
     D = pages.D
     rows, heads = q.shape[0], q.shape[1]
     n_kv = pages.p.shape[1]
@@ -155,6 +158,8 @@ def attention(pages: Pages, q, table, lens, cu, scale, window=0, sinks=0):
                     eps * o.abs() + 2.0 ** -11 * A.abs() + m * 15 * 2.0 ** -31 * sc.abs().max()
                     + (2 * delta + 2.0 ** -17 * (1 + m / 2048)) * (A.abs() + B)
                     + torch.finfo(pages.dtype).smallest_normal * eps)
+                if (r1 - r0) * group > 32:
+                    tol[i, h * group:(h + 1) * group] += 2 * eps * (w @ vv.abs())
     return out, tol
 
 
