@@ -429,10 +429,13 @@ mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64
                                int window, int sinks, void *work, size_t work_bytes,
                                int32_t *status, void *stream);
 
-/* Bytes of `work` for any call with this head_dim on a device of num_sms SMs
- * (num_sms <= 0: the current device; 0 if there is none or head_dim is not
- * supported).  It does not grow with the batch or the lengths. */
-size_t mixq_kv4_attention_workspace_size(int head_dim, int num_sms);
+/* Bytes of `work` for a call whose sequences have at most max_rows rows (new
+ * tokens times n_q_heads / n_kv_heads; 0: no bound) per kv head, on a device of
+ * num_sms SMs (num_sms <= 0: the current device; 0 if there is none or head_dim is
+ * not supported).  A call's bound is max_new (n_rows if that is 0 or larger, 1
+ * without cu) times the heads ratio.  The size does not grow with the batch or the
+ * lengths. */
+size_t mixq_kv4_attention_workspace_size(int head_dim, int max_rows, int num_sms);
 
 /*
  * Test-only: the gemm mainloop alone, raw INT32 accumulators out

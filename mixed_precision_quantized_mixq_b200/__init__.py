@@ -65,7 +65,7 @@ _SIGNATURES = {
     "mixq_kv4_read": (_I, [_VP, _VP, _L, _L, _VP, _L, _L, _I, _I, _VP, _I, _L, _VP, _VP, _VP, _VP]),
     "mixq_kv4_attention": (_I, [_VP, _VP, _L, _L, _VP, _L, _L, _I, _I, _I, _I, _VP, _I, _L, _VP,
                                 _VP, _F, _I, _I, _VP, _SZ, _VP, _VP]),
-    "mixq_kv4_attention_workspace_size": (_SZ, [_I, _I]),
+    "mixq_kv4_attention_workspace_size": (_SZ, [_I, _I, _I]),
     "mixq_debug_gemm_i32": (_I, [_I, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _I, _VP, _VP]),
     "mixq_debug_max_active_clusters": (_I, [_I, _I, _I, _I, _c.POINTER(_I)]),
     "mixq_debug_unpack_w8": (_I, [_I, _I, _VP, _VP, _VP]),
@@ -553,18 +553,22 @@ def kv4_read(cache: KV4Cache, table, cu_rows, rows: int, first=None, k_out=None,
     return k_out, v_out
 
 
-_kv4_work_bytes: dict = {}  # (device index, head_dim) -> bytes
+_kv4_work_bytes: dict = {}  # (device index, head_dim, many rows) -> bytes
+_KV4_STEP_ROWS = 32
 
 
-def kv4_workspace(cache: KV4Cache):
-    """Scratch for kv4_attention (uint8; calls that may overlap on the GPU must not share one)."""
+def kv4_workspace(cache: KV4Cache, max_rows: int = 0):
+    """Scratch for kv4_attention (uint8; calls that may overlap on the GPU must not share one).
+
+    max_rows: a bound on new tokens times n_q_heads / n_kv_heads of one sequence (0: none)."""
     import torch
     dev = cache.pages.device
-    n = _kv4_work_bytes.get((dev.index, cache.head_dim))
+    key = (dev.index, cache.head_dim, not 0 < max_rows <= _KV4_STEP_ROWS)
+    n = _kv4_work_bytes.get(key)
     if n is None:
         with torch.cuda.device(dev):
-            n = lib().mixq_kv4_attention_workspace_size(cache.head_dim, 0)
-        _kv4_work_bytes[dev.index, cache.head_dim] = n
+            n = lib().mixq_kv4_attention_workspace_size(cache.head_dim, max_rows, 0)
+        _kv4_work_bytes[key] = n
     return torch.empty(n, dtype=torch.uint8, device=dev)
 
 
@@ -588,7 +592,8 @@ def kv4_attention(q, cache: KV4Cache, table, seq_lens, cu_new=None, max_new: int
             if out.shape[0] != q.shape[0]:
                 raise MixqError(1, f"out must have {q.shape[0]} rows")
         if work is None:
-            work = kv4_workspace(cache)
+            bound = 1 if cu_new is None else min(max_new, q.shape[0]) if max_new > 0 else q.shape[0]
+            work = kv4_workspace(cache, bound * q.shape[1] // max(1, cache.n_kv_heads))
         elif work.device != cache.pages.device or not work.is_contiguous():
             raise MixqError(1, "work must be contiguous and on the cache's device")
         n, rows, tptr, width, tstride = b

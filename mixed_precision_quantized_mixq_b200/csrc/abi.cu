@@ -547,9 +547,11 @@ static mixq_status kv4_check(const mixq_kv4_cache *c, int n_seqs, int n_rows, co
     return fail(MIXQ_ERR_INVALID_ARG, "table must be non-null");
   if (c->n_pages > 0 && !c->pages) return fail(MIXQ_ERR_INVALID_ARG, "pages must be non-null");
   if (!aligned16(c->pages)) return fail(MIXQ_ERR_MISALIGNED, "pages must be 16-byte aligned");
+  int shift = 0;
+  while ((16 << shift) < c->page_size && shift < 26) ++shift;
   *cache = mixq::Kv4Cache{static_cast<uint8_t *>(c->pages), c->page_stride, c->n_pages,
-                          c->page_size / 16, c->n_kv_heads, c->head_dim,
-                          c->dtype == MIXQ_KV4_BF16};
+                          c->page_size / 16, (16 << shift) == c->page_size ? shift : -1,
+                          c->n_kv_heads, c->head_dim, c->dtype == MIXQ_KV4_BF16};
   *b = mixq::Kv4Batch{n_seqs, table, table_width, table_stride, nullptr, cu, n_rows};
   return MIXQ_OK;
 }
@@ -604,8 +606,15 @@ mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_ro
                    "KV4 read launch");
 }
 
-size_t mixq_kv4_attention_workspace_size(int head_dim, int num_sms) {
-  if (!kv4_dim(head_dim)) return 0;
+// The step kernel's scratch; with more rows than it takes alone, the tile kernel's behind it.
+static size_t kv4_work(int d, int64_t max_rows, int num_sms) {
+  size_t n = mixq::kv4_step_workspace(d, num_sms);
+  if (max_rows > mixq::kKv4TileAbove) n += mixq::kv4_tile_workspace(d, num_sms);
+  return n;
+}
+
+size_t mixq_kv4_attention_workspace_size(int head_dim, int max_rows, int num_sms) {
+  if (!kv4_dim(head_dim) || max_rows < 0) return 0;
   if (num_sms <= 0) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -614,7 +623,7 @@ size_t mixq_kv4_attention_workspace_size(int head_dim, int num_sms) {
     }
     num_sms = mixq::device_sm_count(dev);
   }
-  return num_sms > 0 ? mixq::kv4_attn_workspace(head_dim, num_sms) : 0;
+  return num_sms > 0 ? kv4_work(head_dim, max_rows ? max_rows : 1 << 30, num_sms) : 0;
 }
 
 mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64_t q_row,
@@ -643,9 +652,11 @@ mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64
   if (!work) return fail(MIXQ_ERR_INVALID_ARG, "work must be non-null");
   if (!aligned16(work)) return fail(MIXQ_ERR_MISALIGNED, "work must be 16-byte aligned");
   if ((s = check_device(&a.num_sms)) != MIXQ_OK) return s;
-  if (work_bytes < mixq::kv4_attn_workspace(a.c.d, a.num_sms))
-    return fail(MIXQ_ERR_INVALID_ARG, "work_bytes = %zu must be at least %zu", work_bytes,
-                mixq::kv4_attn_workspace(a.c.d, a.num_sms));
+  a.group = n_q_heads / a.c.n_kv;
+  a.max_rows = static_cast<int64_t>(!cu ? 1 : max_new > 0 && max_new < n_rows ? max_new : n_rows) * a.group;
+  const size_t need = kv4_work(a.c.d, a.max_rows, a.num_sms);
+  if (work_bytes < need)
+    return fail(MIXQ_ERR_INVALID_ARG, "work_bytes = %zu must be at least %zu", work_bytes, need);
   a.b.lens = seq_lens;
   a.q = q;
   a.out = out;
@@ -654,12 +665,11 @@ mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64
   a.o_row = o_row;
   a.o_head = o_head;
   a.n_q = n_q_heads;
-  a.group = n_q_heads / a.c.n_kv;
-  a.max_rows = static_cast<int64_t>(!cu ? 1 : max_new > 0 && max_new < n_rows ? max_new : n_rows) * a.group;
   a.scale = scale;
   a.window = window;
   a.sinks = sinks;
   a.work = static_cast<float *>(work);
+  a.work_tile = a.work + mixq::kv4_step_workspace(a.c.d, a.num_sms) / sizeof(float);
   a.status = status;
   return from_cuda(mixq::launch_kv4_attn(a, static_cast<cudaStream_t>(stream)), "KV4 attention launch");
 }

@@ -20,6 +20,7 @@ struct Kv4Cache {
   int64_t page_stride;  // bytes between pages
   int n_pages;
   int recs_per_page;
+  int page_shift;  // log2(recs_per_page), -1 if that is not a power of two
   int n_kv;
   int d;     // 64 or 128
   int bf16;  // type of the rows and of the (s, lo) pairs
@@ -52,7 +53,8 @@ struct Kv4AttnArgs {
   int64_t tile_above;  // sequences with more rows than this belong to the tile kernel
   float scale;
   int window, sinks;  // window 0: all keys up to the query's position
-  float *work;
+  float *work;       // step kernel's parts
+  float *work_tile;  // tile kernel's parts
   int num_sms;
   int32_t *status;
 };
@@ -61,7 +63,9 @@ cudaError_t launch_kv4_append(const Kv4Cache &c, const Kv4Batch &b, const Kv4Row
                               int32_t *status, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows &r,
                             int32_t *status, cudaStream_t stream);
-size_t kv4_attn_workspace(int d, int num_sms);
+size_t kv4_step_workspace(int d, int num_sms);
+size_t kv4_tile_workspace(int d, int num_sms);
+constexpr int kKv4TileAbove = 32;  // more rows (new tokens x group) of a kv head than this: tile kernel
 // Decode steps and small row counts (kv4_attn.cu), many rows (kv4_tile.cu); the
 // first launches the second where it is needed.
 cudaError_t launch_kv4_attn(Kv4AttnArgs a, cudaStream_t stream);

@@ -38,7 +38,6 @@ constexpr float kNegBig = -1e30f;  // running maximum before the first visible k
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMinQuota = 16;  // records: below two a warp, a cut costs more than it spreads
 constexpr int kMaxRows = 16;
-constexpr int kTileAbove = 32;
 
 struct Desc {  // item whose last part is not in the CTA that starts it
   int seq, item, last, pad;
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     pre.seek(a, pre_i);
     const int rec = pre.record(pre_i);
     if (rec * kKv4Rec >= pre.q.len) return;
-    const int slot = rec / a.c.recs_per_page;
+    const int slot = a.c.page_shift >= 0 ? rec >> a.c.page_shift : rec / a.c.recs_per_page;
     pre_page = __ldg(a.b.table + pre.seq * a.b.table_stride + slot);
     pre_off = (static_cast<int64_t>(pre.head(a)) * a.c.recs_per_page + (rec - slot * a.c.recs_per_page)) * REC;
   };
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
       const float mycs = up * 16777216.f, myqs = up * sum;
       const int p = cur.q.pos0 + qi;
       const int myvis = valid ? min(p + 1, cur.q.len) : 0x7fffffff;
-      const int mywlo = valid && a.window > 0 ? p - a.window + 1 : -0x7fffffff;
+      const int mywlo = valid && a.window > 0 ? max(p, 0) - a.window + 1 : -0x7fffffff;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int src = (2 * t + j) * 4;
@@ -359,6 +358,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     // positions of the tile's first and last row
     const int pmin = cur.q.pos0 + row_first / a.group;
     const int pmax = cur.q.pos0 + (min(row_first + R, rows_all) - 1) / a.group;
+    // keys up to these lie before the window of the first and of the last row (a row at a
+    // negative position sees nothing: 0 stands for it, and no difference leaves 32 bits)
+    const int edge_min = max(pmin, 0) - a.window, edge_max = max(pmax, 0) - a.window;
 
     float o[NT][MT][4], m[NT][2], l[NT][2], z[NT][2];
     float sig = pow2(100);
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
       const uint8_t *rec = sm.ring[warp][slot];
       const bool ok = sm.ok[warp][slot] && !dead;
       const int j0 = cur.record(i) * kKv4Rec;
-      const bool none = !ok || j0 > pmax || (a.window > 0 && j0 + kKv4Rec <= pmin - a.window + 1 && j0 >= a.sinks);
+      const bool none = !ok || j0 > pmax || (a.window > 0 && j0 + kKv4Rec <= edge_min + 1 && j0 >= a.sinks);
       if (!none) {
         uint32_t ka[WORDS], kb[WORDS], vw[WORDS * 2];
         if (D == 128) {
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
           }
         }
         const bool whole = j0 + kKv4Rec <= min(pmin + 1, cur.q.len) &&
-                           (a.window <= 0 || j0 > pmax - a.window || j0 + kKv4Rec <= a.sinks);
+                           (a.window <= 0 || j0 > edge_max || j0 + kKv4Rec <= a.sinks);
         float s0 = v0.x, s1 = v1.x, l0 = v0.y, l1 = v1.y;
         if (!whole) {
 #pragma unroll
@@ -446,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             }
           // tokens that no row of the tile sees may hold anything
           const int k0 = j0 + g, k1 = k0 + 8, last = min(pmax, cur.q.len - 1);
-          if (k0 > last || (a.window > 0 && k0 <= pmin - a.window && k0 >= a.sinks)) s0 = 0.f, l0 = 0.f;
-          if (k1 > last || (a.window > 0 && k1 <= pmin - a.window && k1 >= a.sinks)) s1 = 0.f, l1 = 0.f;
+          if (k0 > last || (a.window > 0 && k0 <= edge_min && k0 >= a.sinks)) s0 = 0.f, l0 = 0.f;
+          if (k1 > last || (a.window > 0 && k1 <= edge_min && k1 >= a.sinks)) s1 = 0.f, l1 = 0.f;
         }
 
         // ---- running maximum, moved only when a score passes it by 2^8
@@ -697,20 +699,20 @@ cudaError_t pick(const Kv4AttnArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t kv4_attn_workspace(int d, int num_sms) {
+size_t kv4_step_workspace(int d, int num_sms) {
   const size_t ctas = 2 * static_cast<size_t>(num_sms);
   return ctas * sizeof(Desc) + ctas * 2 * slot_floats(d) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attn(Kv4AttnArgs a, cudaStream_t stream) {
-  // A sequence with more than kTileAbove rows per kv head goes to the tile kernel; the lengths are
+  // A sequence with more than kKv4TileAbove rows per kv head goes to the tile kernel; the lengths are
   // on the device, so a call whose bound allows both kinds launches both, and each skips the other's.
   a.tile_above = INT64_MAX;
-  if (a.max_rows > kTileAbove) {
-    a.tile_above = kTileAbove;
+  if (a.max_rows > kKv4TileAbove) {
+    a.tile_above = kKv4TileAbove;
     const cudaError_t e = launch_kv4_tile(a, stream);
     if (e != cudaSuccess) return e;
-    a.max_rows = kTileAbove;
+    a.max_rows = kKv4TileAbove;
   }
   if (a.c.bf16)
     return a.c.d == 128 ? pick<__nv_bfloat16, 128>(a, stream) : pick<__nv_bfloat16, 64>(a, stream);

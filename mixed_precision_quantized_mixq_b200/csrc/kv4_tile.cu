@@ -1,10 +1,10 @@
 // Attention over the 4-bit KV cache for many query rows (prompts and chunks of
 // prompts), on the 5th-generation tensor cores.
 //
-// One CTA takes up to 256 query rows of one (sequence, kv head): rows are (new
-// token, head of the group) pairs, so grouped heads fill the tiles.  The rows are
-// two 128-row MMA tiles that take turns: while the softmax of one runs, the
-// tensor core works for the other.  Per 128 keys and row tile
+// Work is up to 256 query rows of one (sequence, kv head) against its visible
+// keys, 128 at a time; rows are (new token, head of the group) pairs, so grouped
+// heads fill the tiles.  The rows are two 128-row MMA tiles that take turns: while
+// the softmax of one runs, the tensor core works for the other.  Per key tile
 //   S = Q C^T   (C: K's codes, exact in the 16-bit type), 128 x 128 x D, in TMEM
 //   t = scale log2(e) (s_k S + lo_k sum(q)),  P = 2^(t - m)
 //   O += P V^   (V^: V's rows as they read back, rounded once to the type)
@@ -16,6 +16,13 @@
 // bytes already in registers), warp 16 issues the MMAs.  K stays in codes because
 // a rounded K would move every score; the pairs act on S instead.  V is rounded
 // to the type like any 16-bit V, which leaves the softmax no work per V row.
+//
+// The key tiles of all (sequence, 256 rows, head) items are one line, cut into
+// equal parts over a persistent grid of one CTA per SM: the load is even whatever
+// the lengths and however few items there are, and the roles run on from item to
+// item, so one item's last softmax and output overlap the next one's first tiles.
+// An item cut by a boundary leaves fp32 partial results, joined by a second launch
+// in the order of the parts.
 //
 // The running maximum moves only when a score passes it by 2^8, so O (in TMEM) is
 // rarely rescaled; P carries 2^6 more so that fp16 keeps 11 bits down to 2^-20 of
@@ -34,12 +41,14 @@ namespace {
 constexpr int kThreads = 640;  // 8 softmax, 8 unpack, 1 MMA warp (and 3 that complete its group)
 constexpr int kRows = 256;     // query rows per CTA
 constexpr int kKeys = 128;     // keys per tile
+constexpr int kSeqChunk = 64;  // sequences the search for a CTA's part looks at together
+constexpr int kMinTiles = 4;   // key tiles per part: below, joining costs more than the cut spreads
 constexpr float kNegBig = -1e30f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// registers per thread after the split; 2*128*176 + 2*128*48 + 128*24 = 60416 of the
-// 640 * 96 = 61440 the CTA starts with
-constexpr int kRegsSoftmax = 176, kRegsUnpack = 48, kRegsMma = 24;
+// registers per thread after the split; 256*128 + 256*80 + 128*64 = 61440, the
+// 640 * 96 the CTA starts with
+constexpr int kRegsSoftmax = 128, kRegsUnpack = 80, kRegsMma = 64;
 
 template <int D>
 struct TileSmem {
@@ -47,8 +56,11 @@ struct TileSmem {
   alignas(1024) uint8_t k[2][kKeys * D * 2];
   alignas(1024) uint8_t v[2][kKeys * D * 2];
   alignas(16) float4 kp[4][kKeys / 2];  // per pair of keys: s0 s1 lo0 lo1, times scale log2(e)
+  alignas(8) uint8_t hidden[4][8];  // records of the tile whose page is not usable
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], par_full[4], s_full[2], p_full[2], o_full[2];
-  uint32_t hidden[4];  // records of the tile whose page is not usable
+  long long cost[kSeqChunk];
+  int found;
+  long long found_start;
   uint32_t tmem;
   int dead;
 };
@@ -119,6 +131,18 @@ __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile in
   }
 }
 
+// The n lowest bits, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  n = min(max(n, 0), 32);
+  return static_cast<uint32_t>((1ull << n) - 1);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <typename T>
 struct Codes;
 template <>
@@ -144,62 +168,95 @@ struct Codes<__nv_bfloat16> {
   }
 };
 
-// The CTA's rows and key tiles.
-struct Job {
-  int seq, row0, len, pos0;  // sequence, its first q row, its keys, position of its first new token
-  int first, rows;           // rows of the kv head: first of this CTA, how many
-  int tiles;                 // key tiles to visit
-  int sink_tiles, skip;      // tile i >= sink_tiles is key tile i + skip
-  __device__ __forceinline__ int key0(int i) const {
-    return (i + (i >= sink_tiles ? skip : 0)) * kKeys;
-  }
+// A sequence as the walk sees it.
+struct Rows {
+  int row0, len, pos0;  // first q row, keys that exist, position of the first new token
+  int rows;             // query rows of a kv head
+  int blocks;           // of 256 rows; 0: the sequence is not this kernel's
 };
 
-// Virtual row tile v belongs to the last sequence s with floor(cu[s] G / 256) + s
-// <= v: every sequence owns at least as many as its rows fill, and the search
-// needs cu alone.  A sequence's last rows come first (they see the most keys).
-// rows == 0: nothing to do.
-__device__ __forceinline__ Job find_job(const Kv4AttnArgs &a, int v, int lane) {
-  Job j{};
-  int lo = 0, hi = a.b.n_seqs - 1;
-  while (lo < hi) {
-    const int step = (hi - lo + 31) / 32;
-    const int s = min(lo + (lane + 1) * step, hi);
-    const int64_t row = a.b.cu ? __ldg(a.b.cu + s) : s;
-    const int64_t start = row * a.group / kRows + s;
-    const int k = __popc(__ballot_sync(0xffffffffu, start <= v));
-    const int nlo = min(lo + k * step, hi);
-    hi = k == 32 ? hi : max(nlo, min(lo + (k + 1) * step - 1, hi));
-    lo = nlo;
-  }
+__device__ __forceinline__ Rows load_rows(const Kv4AttnArgs &a, int s) {
+  Rows q{};
   bool bad = false;
-  const int2 r = kv4_row_range(a.b, lo, &bad);
-  const int full = __ldg(a.b.lens + lo);
+  const int2 r = kv4_row_range(a.b, s, &bad);
+  const int full = __ldg(a.b.lens + s);
   const int64_t cap = static_cast<int64_t>(a.b.table_width) * a.c.recs_per_page * kKv4Rec;
-  if (threadIdx.x == 0 && (bad || full < 0 || full > cap)) record_error(a.status, kErrInvalidArg);
-  if (bad) return j;
-  const int64_t all = static_cast<int64_t>(r.y - r.x) * a.group;
-  const int n_tiles = static_cast<int>((all + kRows - 1) / kRows);
-  const int64_t local = v - (static_cast<int64_t>(r.x) * a.group / kRows + lo);
-  if (all <= a.tile_above || local < 0 || local >= n_tiles) return j;
-  j.seq = lo;
-  j.row0 = r.x;
-  j.first = static_cast<int>(n_tiles - 1 - local) * kRows;
-  j.rows = static_cast<int>(min(static_cast<int64_t>(kRows), all - j.first));
-  j.len = static_cast<int>(min(static_cast<int64_t>(max(full, 0)), cap));
-  j.pos0 = full - (r.y - r.x);
-  const int pmin = j.pos0 + j.first / a.group, pmax = j.pos0 + (j.first + j.rows - 1) / a.group;
-  const int total = (max(0, min(j.len, pmax + 1)) + kKeys - 1) / kKeys;
-  j.sink_tiles = total;
-  j.tiles = total;
-  if (a.window > 0) {
-    const int w0 = min(max(0, max(pmin, 0) - a.window + 1) / kKeys, total);
-    j.sink_tiles = min((min(a.sinks, j.len) + kKeys - 1) / kKeys, w0);
-    j.skip = w0 - j.sink_tiles;
-    j.tiles = total - j.skip;
-  }
-  return j;
+  if ((threadIdx.x & 31) == 0 && (bad || full < 0 || full > cap)) record_error(a.status, kErrInvalidArg);
+  q.row0 = r.x;
+  q.len = static_cast<int>(min(static_cast<int64_t>(max(full, 0)), cap));
+  q.pos0 = full - (r.y - r.x);
+  q.rows = (r.y - r.x) * a.group;
+  q.blocks = q.rows > a.tile_above ? (q.rows + kRows - 1) / kRows : 0;
+  return q;
 }
+
+// The key tiles that a block of rows visits: tile i is key tile i, from `sinks` on i + skip.
+struct Keys {
+  int tiles, sinks, skip;
+  __device__ __forceinline__ int key0(int i) const { return (i + (i >= sinks ? skip : 0)) * kKeys; }
+};
+
+__device__ __forceinline__ Keys keys_of(const Kv4AttnArgs &a, const Rows &q, int block) {
+  const int first = block * kRows, last = min(first + kRows, q.rows) - 1;
+  const int total = (max(0, min(q.len, q.pos0 + last / a.group + 1)) + kKeys - 1) / kKeys;
+  Keys k{total, total, 0};
+  if (a.window > 0) {
+    const int w0 = min(max(0, max(q.pos0 + first / a.group, 0) - a.window + 1) / kKeys, total);
+    k.sinks = min((min(a.sinks, q.len) + kKeys - 1) / kKeys, w0);
+    k.skip = w0 - k.sinks;
+    k.tiles = total - k.skip;
+  }
+  k.tiles = max(k.tiles, 1);  // rows that see nothing still get their zeros, from a tile without keys
+  return k;
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Key tiles of sequence s over all its blocks and heads (whole warp).
+__device__ __forceinline__ long long seq_tiles(const Kv4AttnArgs &a, int s, int lane) {
+  const Rows q = load_rows(a, s);
+  long long n = 0;
+  for (int b = lane; b < q.blocks; b += 32) n += keys_of(a, q, b).tiles;
+  return warp_sum(n) * a.c.n_kv;
+}
+
+// A CTA's part of the line, one item after another.
+struct Walk {
+  Rows q;
+  Keys k;
+  int seq, block, head;
+  int t0, t1;  // tiles of the item that belong to the part
+  int left;    // tiles of the part from t0 on
+
+  __device__ __forceinline__ void set() { t1 = min(k.tiles, t0 + left); }
+  __device__ __forceinline__ bool more() const { return left > t1 - t0; }
+  __device__ __forceinline__ void next(const Kv4AttnArgs &a) {
+    left -= t1 - t0;
+    t0 = 0;
+    if (++head == a.c.n_kv) {
+      head = 0;
+      if (++block >= q.blocks) {
+        block = 0;
+        do {
+          q = load_rows(a, ++seq);
+        } while (q.blocks == 0);
+      }
+      k = keys_of(a, q, block);
+    }
+    set();
+  }
+  __device__ __forceinline__ int rows() const { return min(kRows, q.rows - block * kRows); }
+};
+
+struct Desc {  // item whose last part is not in the CTA that starts it
+  int seq, block, head, last;
+};
+
+__host__ __device__ constexpr size_t slot_floats(int d) { return kRows * (static_cast<size_t>(d) + 2); }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs a) {
@@ -211,12 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   S &sm = *reinterpret_cast<S *>(smem_raw);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-  const int head = blockIdx.x;
 
-  griddep_wait();
-  griddep_launch_dependents();
-  const Job job = find_job(a, blockIdx.y, lane);
-  if (job.rows == 0) return;
   if (tid == 0) {
     sm.dead = 0;
     for (int i = 0; i < 2; ++i) {
@@ -229,198 +281,350 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.o_full[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.par_full[i], 8);
-      sm.hidden[i] = 0;
-    }
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.par_full[i], 8);
     fence_mbar_init();
   }
   if (warp == 16) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- this CTA's part [lo, lo + mylen) of the line
+  long long total = 0;
+  for (int s0 = 0; s0 < a.b.n_seqs; s0 += kSeqChunk) {
+    __syncthreads();
+    for (int s = warp; s < kSeqChunk; s += kThreads / 32) {
+      const long long c = s0 + s < a.b.n_seqs ? seq_tiles(a, s0 + s, lane) : 0;
+      if (lane == 0) sm.cost[s] = c;
+    }
+    __syncthreads();
+    total += warp_sum(sm.cost[lane] + sm.cost[lane + 32]);
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long quota = max(per, static_cast<long long>(kMinTiles));
+  const long long lo = min(static_cast<long long>(blockIdx.x) * quota, total);
+  const int mylen = static_cast<int>(min(quota, total - lo));
+  Desc *desc = reinterpret_cast<Desc *>(a.work_tile);
+  float *slots = a.work_tile + gridDim.x * (sizeof(Desc) / 4);
+  if (tid == 0) desc[blockIdx.x].seq = -1;
+  Walk w{};
+  if (mylen > 0) {
+    long long base = 0;
+    for (int s0 = 0; s0 < a.b.n_seqs; s0 += kSeqChunk) {
+      if (a.b.n_seqs > kSeqChunk) {  // else the costs are there
+        __syncthreads();
+        for (int s = warp; s < kSeqChunk; s += kThreads / 32) {
+          const long long c = s0 + s < a.b.n_seqs ? seq_tiles(a, s0 + s, lane) : 0;
+          if (lane == 0) sm.cost[s] = c;
+        }
+        __syncthreads();
+      }
+      if (tid == 0) {
+        sm.found = -1;
+        long long at = base;
+        for (int s = 0; s < kSeqChunk; ++s) {
+          if (lo >= at && lo < at + sm.cost[s]) {
+            sm.found = s0 + s;
+            sm.found_start = at;
+          }
+          at += sm.cost[s];
+        }
+      }
+      base += warp_sum(sm.cost[lane] + sm.cost[lane + 32]);
+      __syncthreads();
+      if (sm.found >= 0) break;
+    }
+    w.seq = sm.found;
+    w.q = load_rows(a, w.seq);
+    // the block: its heads' tiles begin at or before lo and end after it
+    long long in = lo - sm.found_start, at = 0;
+    for (int b0 = 0; b0 < w.q.blocks; b0 += 32) {
+      const long long c = b0 + lane < w.q.blocks ? static_cast<long long>(keys_of(a, w.q, b0 + lane).tiles) * a.c.n_kv : 0;
+      long long incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, in < at + incl);
+      if (hit) {
+        const int f = __ffs(hit) - 1;
+        w.block = b0 + f;
+        in -= at + __shfl_sync(0xffffffffu, incl - c, f);
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    w.k = keys_of(a, w.q, w.block);
+    w.head = static_cast<int>(in / w.k.tiles);
+    w.t0 = static_cast<int>(in - static_cast<long long>(w.head) * w.k.tiles);
+    w.left = mylen;
+    w.set();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + D};
-  const int row_tiles = job.rows > 128 ? 2 : 1;
-  const int n = job.tiles;
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax
     reg_inc<kRegsSoftmax>();
     const int i = warp / 4, row = tid & 127, r = i * 128 + row;
-    if (i < row_tiles) {
-      const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes per warp
-      const bool valid = r < job.rows;
-      const int qi = (job.first + r) / a.group, g = job.first + r - qi * a.group;
-      const int64_t head_q = static_cast<int64_t>(head) * a.group + g;
-      const int p = job.pos0 + qi;
-      // ---- the thread's query row into the operand tile, and its sum
-      float qsum = 0.f;
-      {
-        const T *qp = static_cast<const T *>(a.q) + (job.row0 + static_cast<int64_t>(qi)) * a.q_row + head_q * a.q_head;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes per warp
+    int jt = 0;              // key tiles of the CTA so far
+    int jn = 0;              // those of this row tile (its barriers' phases)
+    float qsum = 0.f;
+    // the thread's query row into the operand tile, and its sum
+    auto load_q = [&]() {
+      if (i * 128 >= w.rows()) return;
+      const int rr = w.block * kRows + r, qi = rr / a.group;
+      const bool valid = r < w.rows();
+      const T *qp = static_cast<const T *>(a.q) + (w.q.row0 + static_cast<int64_t>(qi)) * a.q_row +
+                    (static_cast<int64_t>(w.head) * a.group + (rr - qi * a.group)) * a.q_head;
+      qsum = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c) : make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = X::f2(kv4_bits<T2>(u[e]));
-            qsum += f.x;
-            qsum += f.y;
-          }
-          *reinterpret_cast<uint4 *>(sm.q[i] + (c / 8) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x;
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = X::f2(kv4_bits<T2>(u[e]));
+          qsum += f.x;
+          qsum += f.y;
         }
-        fence_proxy_async_smem();
-        mbar_arrive(&sm.q_full[i]);
+        *reinterpret_cast<uint4 *>(sm.q[i] + (c / 8) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x;
       }
-      const uint64_t qs2 = pack2(qsum, qsum);
+      fence_proxy_async_smem();
+      mbar_arrive(&sm.q_full[i]);
+    };
+    if (mylen > 0) load_q();
+    bool go = mylen > 0;
+#pragma unroll 1
+    while (go) {
+      const int rows = w.rows(), first = w.block * kRows, n = w.t1 - w.t0;
+      const bool active = i * 128 < rows, valid = r < rows;
+      const int qi = (first + r) / a.group;
+      const int64_t head_q = static_cast<int64_t>(w.head) * a.group + (first + r - qi * a.group);
+      const int64_t orow = w.q.row0 + static_cast<int64_t>(qi);
       // key j is visible when j < vis and (j >= wlo or j < sinks)
-      const int vis = valid ? min(p + 1, job.len) : job.len;
-      const int wlo = valid && a.window > 0 ? p - a.window + 1 : -0x7fffffff;
-      const int tmin = job.pos0 + (job.first + i * 128) / a.group;
-      const int tmax = job.pos0 + (job.first + min(i * 128 + 128, job.rows) - 1) / a.group;
-      float m = kNegBig;
-      uint64_t l2 = pack2(0.f, 0.f);
+      const int vis = valid ? min(w.q.pos0 + qi + 1, w.q.len) : w.q.len;
+      const int wlo = valid && a.window > 0 ? max(max(w.q.pos0 + qi, 0) - a.window + 1, 0) : 0;
+      const int tmin = min(w.q.pos0 + (first + i * 128) / a.group + 1, w.q.len);
+      const int tmax = max(w.q.pos0 + (first + min(i * 128 + 128, rows) - 1) / a.group, 0);
+      const Keys keys = w.k;
+      const int t0 = w.t0;
+      const bool begins = w.t0 == 0, ends = w.t1 == w.k.tiles;
+      float base = 0.f;            // what is added to t: 6 - m once a key was seen
+      float limit = -INFINITY;     // t + base above this moves the maximum
+      uint64_t la = pack2(0.f, 0.f), lb = la;
+      const uint64_t qs2 = pack2(qsum, qsum);
+
+      if (active) {
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        const int k0 = job.key0(j);
-        wait(&sm.par_full[j & 3], (j >> 2) & 1, &sm.dead, a.status);
-        const float4 *kp = sm.kp[j & 3];
-        const uint32_t hid = sm.hidden[j & 3];
-        wait(&sm.s_full[i], j & 1, &sm.dead, a.status);
-        tc_fence_after();
-        union {
-          uint32_t u[4][32];
-          float f[128];
-          uint64_t d[64];
-        } t;
+        for (int j = 0; j < n; ++j) {
+          const int k0 = keys.key0(t0 + j), st = (jt + j) & 3;
+          wait(&sm.par_full[st], ((jt + j) >> 2) & 1, &sm.dead, a.status);
+          const float4 *kp = sm.kp[st];
+          const uint2 hid = *reinterpret_cast<const uint2 *>(sm.hidden[st]);
+          const bool whole = (hid.x | hid.y) == 0 && k0 + kKeys <= tmin &&
+                             (a.window <= 0 || k0 > tmax - a.window || k0 + kKeys <= a.sinks);
+          wait(&sm.s_full[i], (jn + j) & 1, &sm.dead, a.status);
+          tc_fence_after();
+          union Chunk {
+            uint32_t u[32];
+            float f[32];
+            uint64_t d[16];
+          } buf[2];
+          // t + base of 32 keys in place of their scores, and the largest
+          auto scores = [&](Chunk &t, int c) -> float {
+            const uint64_t b2 = pack2(base, base);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tm_s[i] + lanes + c * 32, t.u[c]);
-        tmem_ld_wait();
+            for (int e = 0; e < 16; ++e) {
+              const float4 x = kp[c * 16 + e];
+              t.d[e] = fma2(t.d[e], pack2(x.x, x.y), fma2(pack2(x.z, x.w), qs2, b2));
+            }
+            if (!whole) {
+              // one bit per key, so that no lane branches
+              const int kc = k0 + c * 32;
+              const uint32_t off = (c < 2 ? hid.x : hid.y) >> ((c & 1) * 16);
+              const uint32_t seen = low_bits(vis - kc) & (~low_bits(wlo - kc) | low_bits(a.sinks - kc)) &
+                                    ~((off & 1u) * 0xffffu | (off >> 8 & 1u) * 0xffff0000u);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const float4 x = kp[c];
-          t.d[c] = fma2(t.d[c], pack2(x.x, x.y), mul2(pack2(x.z, x.w), qs2));
-        }
-        const bool whole = hid == 0 && k0 + kKeys <= min(tmin + 1, job.len) &&
-                           (a.window <= 0 || k0 > tmax - a.window || k0 + kKeys <= a.sinks);
-        if (!whole) {
+              for (int e = 0; e < 32; ++e) t.f[e] = seen & (1u << e) ? t.f[e] : -INFINITY;
+            }
+            float m0 = max3(t.f[0], t.f[1], t.f[2]), m1 = max3(t.f[3], t.f[4], t.f[5]);
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const int key = k0 + c;
-            if (key >= vis || (key < wlo && key >= a.sinks) || (hid >> (c / 16) & 1)) t.f[c] = -INFINITY;
-          }
-        }
-        float mx = t.f[0];
+            for (int e = 6; e < 30; e += 4) {
+              m0 = max3(m0, t.f[e], t.f[e + 1]);
+              m1 = max3(m1, t.f[e + 2], t.f[e + 3]);
+            }
+            return max3(m0, m1, fmaxf(t.f[30], t.f[31]));
+          };
+          // moves the maximum: the chunk, and what the row has in O, the sums and this tile's
+          // first c chunks of weights
+          auto grow = [&](Chunk &t, int c, float mx) {
+            const bool need = mx > limit;
+            const float d = need ? 6.f - mx : 0.f;
+            const float al = limit > -INFINITY ? ex2f(d) : 1.f;  // nothing to scale before the first key
+            if (need) limit = 14.f;
+            base += d;
+            const uint64_t d2 = pack2(d, d), al2 = pack2(al, al);
 #pragma unroll
-        for (int c = 1; c < 128; ++c) mx = fmaxf(mx, t.f[c]);
-        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-          const float nm = fmaxf(m, mx);
-          const float al = ex2f(m - nm);
-          m = nm;
-          l2 = mul2(l2, pack2(al, al));
-          if (j > 0) {
-            wait(&sm.o_full[i], (j - 1) & 1, &sm.dead, a.status);
-            tc_fence_after();
+            for (int e = 0; e < 16; ++e) t.d[e] = add2(t.d[e], d2);
+            la = mul2(la, al2);
+            lb = mul2(lb, al2);
+            if (j > 0) {
+              wait(&sm.o_full[i], (jn + j - 1) & 1, &sm.dead, a.status);
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(tm_o[i] + lanes + c * 16, o);
-              tmem_ld_wait();
+              for (int x = 0; x < D / 16; ++x) {
+                uint32_t o[16];
+                tmem_ld16(tm_o[i] + lanes + x * 16, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-              tmem_st16(tm_o[i] + lanes + c * 16, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                tmem_st16(tm_o[i] + lanes + x * 16, o);
+              }
+            }
+            if (c > 0) {
+              tmem_st_wait();
+#pragma unroll 1
+              for (int x = 0; x < c; ++x) {
+                uint32_t o[16];
+                tmem_ld16(tm_s[i] + lanes + x * 16, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float2 f = X::f2(kv4_bits<T2>(o[e]));
+                  o[e] = kv4_bits<uint32_t>(X::from2(f.x * al, f.y * al));
+                }
+                tmem_st16(tm_s[i] + lanes + x * 16, o);
+              }
             }
             tmem_st_wait();
-          }
-        }
-        const uint64_t shift = pack2(6.f - m, 6.f - m);
+          };
+          // 32 keys at a time: the exponentials of one chunk beside the scores of the next.  P of
+          // keys [32c, 32c + 32) takes TMEM columns [16c, 16c + 16), whose scores have been read.
+          tmem_ld32(tm_s[i] + lanes, buf[0].u);
+          tmem_ld_wait();
+          tmem_ld32(tm_s[i] + lanes + 32, buf[1].u);
+          float mx = scores(buf[0], 0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+          for (int c = 0; c < 4; ++c) {
+            Chunk &t = buf[c & 1];
+            if (__any_sync(0xffffffffu, mx > limit)) grow(t, c, mx);
+            if (c < 3) tmem_ld_wait();
+            uint32_t p[16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float2 x = unpack2(add2(t.d[h * 32 + c], shift));
-            const float p0 = ex2f(x.x), p1 = ex2f(x.y);
-            l2 = add2(l2, pack2(p0, p1));
-            w[c] = kv4_bits<uint32_t>(X::from2(p0, p1));
+            for (int e = 0; e < 16; ++e) {
+              const float2 x = unpack2(t.d[e]);
+              const float p0 = ex2f(x.x), p1 = ex2f(x.y);
+              if (e & 1) lb = add2(lb, pack2(p0, p1));
+              else la = add2(la, pack2(p0, p1));
+              p[e] = kv4_bits<uint32_t>(X::from2(p0, p1));
+            }
+            if (c < 3) mx = scores(buf[(c + 1) & 1], c + 1);
+            tmem_st16(tm_s[i] + lanes + c * 16, p);
+            if (c < 2) tmem_ld32(tm_s[i] + lanes + (c + 2) * 32, t.u);
           }
-          tmem_st32(tm_s[i] + lanes + h * 32, w);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[i]);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[i]);
+        jn += n;
       }
-      // ---- the row's result.  Column c of O is dim 2c, column D/2 + c dim 2c + 1.
-      float inv = 0.f;
-      if (n > 0) {
-        const float2 l = unpack2(l2);
-        const float sum = l.x + l.y;
-        inv = sum == 0.f ? 0.f : 1.f / sum;
-        wait(&sm.o_full[i], (n - 1) & 1, &sm.dead, a.status);
+      jt += n;
+      // ---- on to the next item's queries, then this one's result.  Column c of O is dim 2c,
+      // column D/2 + c dim 2c + 1.
+      go = w.more();
+      if (go) {
+        w.next(a);
+        load_q();
+      } else if (warp == 0 && lane == 0 && begins && !ends) {
+        const long long end = lo + mylen + (keys.tiles - (t0 + n));
+        desc[blockIdx.x] = Desc{w.seq, w.block, w.head, static_cast<int>((end - 1) / quota)};
+      }
+      if (active) {
+        const float2 l0 = unpack2(la), l1 = unpack2(lb);
+        const float sum = (l0.x + l0.y) + (l1.x + l1.y);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        wait(&sm.o_full[i], (jn - 1) & 1, &sm.dead, a.status);
         tc_fence_after();
-      }
-      T *op = static_cast<T *>(a.out) + (job.row0 + static_cast<int64_t>(qi)) * a.o_row + head_q * a.o_head;
+        const bool full = begins && ends;
+        float *part = slots + (2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0)) * slot_floats(D);
+        T *op = static_cast<T *>(a.out) + orow * a.o_row + head_q * a.o_head;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t e0[16], e1[16];
-        if (n > 0) {
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t e0[16], e1[16];
           tmem_ld16(tm_o[i] + lanes + c * 16, e0);
           tmem_ld16(tm_o[i] + lanes + D / 2 + c * 16, e1);
           tmem_ld_wait();
-        } else {
+          if (valid && full) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) e0[e] = e1[e] = 0;
+            for (int e = 0; e < 4; ++e) {
+              uint32_t x[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                x[y] = kv4_bits<uint32_t>(X::from2(__uint_as_float(e0[4 * e + y]) * inv, __uint_as_float(e1[4 * e + y]) * inv));
+              reinterpret_cast<uint4 *>(op)[c * 4 + e] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4 *>(part + r * D)[c * 8 + e] = make_uint4(e0[2 * e], e1[2 * e], e0[2 * e + 1], e1[2 * e + 1]);
+          }
         }
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = kv4_bits<uint32_t>(X::from2(__uint_as_float(e0[e]) * inv, __uint_as_float(e1[e]) * inv));
-        if (valid) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint4 *>(op)[c * 4 + e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        if (valid && !full) {
+          part[kRows * D + r] = limit > -INFINITY ? -base : kNegBig;
+          part[kRows * D + kRows + r] = sum;
         }
+        tc_fence_before();
       }
-      tc_fence_before();
     }
   } else if (warp < 16) {
     // -------------------------------------------------------------- unpack
     reg_dec<kRegsUnpack>();
     const int rw = warp - 8, g = lane >> 2, t = lane & 3;
     const float sl2 = a.scale * 1.4426950408889634f;
-    const uint8_t *base = a.c.pages + static_cast<int64_t>(head) * a.c.recs_per_page * REC;
-    const int32_t *table = a.b.table + job.seq * a.b.table_stride;
     uint4 k[2], v[D / 64];
     uint32_t pr = 0;  // lane's (s, lo): token lane % 16, of K below lane 16 and V above
     int state = 0;    // of the loaded record: 0 beyond the keys, 1 loaded, 2 page not usable
-    int page = -1;
-    auto load_page = [&](int j) {
+    // two steps ahead of the unpacking: the page of a record, one turn later its bytes
+    int pj = 0;        // next tile of w whose page is asked for
+    int page = -1;     // -1: beyond the keys
+    int64_t off = 0;   // of the record in its page
+    bool any = mylen > 0;
+    auto ask = [&]() {
       page = -1;
-      if (j >= n) return;
-      const int key = job.key0(j) + rw * 16;
-      if (key < job.len) page = __ldg(table + key / 16 / a.c.recs_per_page);
+      off = -1;
+      if (!any) return;
+      if (pj == w.t1 - w.t0) {
+        any = w.more();
+        if (!any) return;
+        w.next(a);
+        pj = 0;
+      }
+      const int key = w.k.key0(w.t0 + pj) + rw * 16;
+      ++pj;
+      if (key >= w.q.len) return;
+      const int rec = key / 16;
+      const int slot = a.c.page_shift >= 0 ? rec >> a.c.page_shift : rec / a.c.recs_per_page;
+      page = __ldg(a.b.table + w.seq * a.b.table_stride + slot);
+      off = (static_cast<int64_t>(w.head) * a.c.recs_per_page + (rec - slot * a.c.recs_per_page)) * REC;
     };
-    auto load = [&](int j) {
+    auto load = [&]() {
       k[0] = k[1] = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) v[c] = make_uint4(0, 0, 0, 0);
       pr = 0;
-      state = 0;
-      if (j >= n) return;
-      const int key = job.key0(j) + rw * 16;
-      if (key >= job.len) return;
-      if (page < 0 || page >= a.c.n_pages) {
-        state = 2;
-        if (lane == 0) record_error(a.status, kErrInvalidArg);
-        return;
-      }
-      state = 1;
-      const uint8_t *rec = base + page * a.c.page_stride + (key / 16 % a.c.recs_per_page) * REC;
+      state = off < 0 ? 0 : page < 0 || page >= a.c.n_pages ? 2 : 1;
+      if (state == 2 && lane == 0) record_error(a.status, kErrInvalidArg);
+      if (state != 1) return;
+      const uint8_t *rec = a.c.pages + page * a.c.page_stride + off;
       if (D == 128) {
         k[0] = __ldg(reinterpret_cast<const uint4 *>(rec) + lane);
         k[1] = __ldg(reinterpret_cast<const uint4 *>(rec + 512) + lane);
@@ -433,15 +637,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       for (int c = 0; c < D / 64; ++c) v[c] = __ldg(reinterpret_cast<const uint4 *>(rec + 8 * D + c * 512) + lane);
       pr = __ldg(reinterpret_cast<const uint32_t *>(rec + 16 * D) + lane);
     };
-    load_page(0);
-    load(0);
-    load_page(1);
+    ask();
+    load();
+    ask();
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; j < mylen; ++j) {
       const int st = j & 1;
       // pairs: a row whose own K or V pair is not finite scores NaN and has V = 0, so that
       // only queries that see it become NaN
-      float2 own = kv4_pair<BF>(pr);
+      const float2 own = kv4_pair<BF>(pr);
       const bool fin = (own.x + own.y) - (own.x + own.y) == 0.f;
       const bool both = __shfl_xor_sync(0xffffffffu, static_cast<int>(fin), 16) && fin;
       if (j >= 2) wait(&sm.k_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
@@ -450,30 +654,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         kp[0] = both ? own.x * sl2 : 0.f;
         kp[2] = both ? own.y * sl2 : NAN;
       }
-      if (state == 2 && lane == 0) atomicOr(&sm.hidden[j & 3], 1u << rw);
-      if (state != 2 && lane == 0) atomicAnd(&sm.hidden[j & 3], ~(1u << rw));
+      if (lane == 0) sm.hidden[j & 3][rw] = state == 2;
       // ---- K codes: lane (g, t) has dims [t D/4, (t+1) D/4) of keys g and g + 8
-      uint8_t *kt = sm.k[st];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int key = rw * 16 + h * 8 + g;
-        uint32_t w[WORDS];
+        uint8_t *kt = sm.k[st] + (rw * 16 + h * 8 + g) * 128;
+        uint32_t word[WORDS];
         if (D == 128) {
-          w[0] = k[h].x, w[1] = k[h].y, w[WORDS - 2] = k[h].z, w[WORDS - 1] = k[h].w;
+          // lanes t >= 2 take their words in another order: eight lanes of a 16-byte store then
+          // hit eight different 16-byte banks
+          const bool swap = t & 2;
+          word[0] = swap ? k[h].z : k[h].x, word[1] = swap ? k[h].w : k[h].y;
+          word[WORDS - 2] = swap ? k[h].x : k[h].z, word[WORDS - 1] = swap ? k[h].y : k[h].w;
         } else {
-          w[0] = h ? k[0].z : k[0].x, w[1] = h ? k[0].w : k[0].y;
+          word[0] = h ? k[0].z : k[0].x, word[1] = h ? k[0].w : k[0].y;
         }
 #pragma unroll
         for (int x = 0; x < WORDS; ++x) {
-          // lanes t >= 2 take their words in another order: eight lanes of a 16-byte store then hit
-          // eight different 16-byte banks
-          const int y = D == 128 ? x ^ (t & 2) : x;
-          uint32_t word = w[x];
-          if (D == 128) word = (t & 2) ? w[x ^ 2] : w[x];
           T2 c[4];
-          Codes<T>::pairs(word, c);
-          const int chunk = t * WORDS + y;  // 16-byte chunk of the row: 8 dims
-          *reinterpret_cast<uint4 *>(kt + (chunk / 8) * 16384 + key * 128 + (((chunk & 7) ^ g) << 4)) =
+          Codes<T>::pairs(word[x], c);
+          const int chunk = t * WORDS + (D == 128 ? x ^ (t & 2) : x);  // 16-byte chunk of the row: 8 dims
+          *reinterpret_cast<uint4 *>(kt + (chunk / 8) * 16384 + (((chunk & 7) ^ g) << 4)) =
               make_uint4(kv4_bits<uint32_t>(c[0]), kv4_bits<uint32_t>(c[1]), kv4_bits<uint32_t>(c[2]),
                          kv4_bits<uint32_t>(c[3]));
         }
@@ -495,39 +696,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         const T2 s0 = kv4_bits<T2>(__byte_perm(q[0], q[1], 0x5410)), l0 = kv4_bits<T2>(__byte_perm(q[0], q[1], 0x7632));
         const T2 s1 = kv4_bits<T2>(__byte_perm(q[2], q[3], 0x5410)), l1 = kv4_bits<T2>(__byte_perm(q[2], q[3], 0x7632));
         const T2 top = X::from2(X::max_finite, X::max_finite);
-        uint8_t *vt = sm.v[st] + (rw / 4) * (D * 128) + 4 * t;
         const int c0 = (rw & 3) * 2;  // chunk of tokens 0..7 of the record
+        uint8_t *v0 = sm.v[st] + (rw / 4) * (D * 128) + g * 128 + 4 * t + ((c0 ^ g) << 4);
+        uint8_t *v1 = sm.v[st] + (rw / 4) * (D * 128) + g * 128 + 4 * t + (((c0 + 1) ^ g) << 4);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+          const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int e = 0; e < 4; ++e) {
             T2 o[4];  // (dim 2b, tokens 2t..), (2b + 1, 2t..), (2b, 2t+8..), (2b + 1, 2t+8..)
-            Codes<T>::pairs(w[x], o);
-            uint8_t *row = vt + (c * 32 + x * 8 + g) * 128;
-            const int at0 = (c0 ^ g) << 4, at1 = ((c0 + 1) ^ g) << 4;
+            Codes<T>::pairs(x[e], o);
+            const int at = (c * 32 + e * 8) * 128;
             // 15 s + lo can pass the type's largest value (s is rounded): hold it there
-            *reinterpret_cast<T2 *>(row + at0) = __hmin2(__hfma2(o[0], s0, l0), top);
-            *reinterpret_cast<T2 *>(row + D * 64 + at0) = __hmin2(__hfma2(o[1], s0, l0), top);
-            *reinterpret_cast<T2 *>(row + at1) = __hmin2(__hfma2(o[2], s1, l1), top);
-            *reinterpret_cast<T2 *>(row + D * 64 + at1) = __hmin2(__hfma2(o[3], s1, l1), top);
+            *reinterpret_cast<T2 *>(v0 + at) = __hmin2(__hfma2(o[0], s0, l0), top);
+            *reinterpret_cast<T2 *>(v0 + at + D * 64) = __hmin2(__hfma2(o[1], s0, l0), top);
+            *reinterpret_cast<T2 *>(v1 + at) = __hmin2(__hfma2(o[2], s1, l1), top);
+            *reinterpret_cast<T2 *>(v1 + at + D * 64) = __hmin2(__hfma2(o[3], s1, l1), top);
           }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[st]);
-      load(j + 1);
-      load_page(j + 2);
+      load();
+      ask();
     }
   } else {
     // ----------------------------------------------------------------- MMA
     reg_dec<kRegsMma>();
-    if (warp == 16 && lane == 0 && n > 0) {
+    if (warp == 16 && lane == 0 && mylen > 0) {
       constexpr uint32_t kind = BF ? (1u << 7) | (1u << 10) : 0u;
       constexpr uint32_t id_qk = idesc_f16_f32(128, kKeys) | kind, id_pv = idesc_f16_f32(128, D) | kind;
-      auto qk = [&](int i, int j) {
-        const uint64_t qd = sw128_kmajor_desc(smem_u32(sm.q[i])), kd = sw128_kmajor_desc(smem_u32(sm.k[j & 1]));
+      auto qk = [&](int i, int jt) {
+        const uint64_t qd = sw128_kmajor_desc(smem_u32(sm.q[i])), kd = sw128_kmajor_desc(smem_u32(sm.k[jt & 1]));
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
           const uint64_t adv = (x / 4) * (16384 >> 4) + (x % 4) * 2;
@@ -535,39 +736,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         }
         mma_commit(&sm.s_full[i]);
       };
-      auto pv = [&](int i, int j) {
-        const uint64_t vd = sw128_kmajor_desc(smem_u32(sm.v[j & 1]));
+      auto pv = [&](int i, int jt, bool add) {
+        const uint64_t vd = sw128_kmajor_desc(smem_u32(sm.v[jt & 1]));
 #pragma unroll
         for (int x = 0; x < kKeys / 16; ++x) {
           const uint64_t adv = (x / 4) * ((D * 128) >> 4) + (x % 4) * 2;
-          mma_f16_ts(tm_o[i], tm_s[i] + x * 8, vd + adv, id_pv, j > 0 || x > 0);
+          mma_f16_ts(tm_o[i], tm_s[i] + x * 8, vd + adv, id_pv, add || x > 0);
         }
         mma_commit(&sm.o_full[i]);
       };
-      wait(&sm.k_full[0], 0, &sm.dead, a.status);
-      for (int i = 0; i < row_tiles; ++i) {
-        wait(&sm.q_full[i], 0, &sm.dead, a.status);
-        tc_fence_after();
-        qk(i, 0);
-      }
-      mma_commit(&sm.k_empty[0]);
+      int jt = 0, jn0 = 0, jn1 = 0, it0 = 0, it1 = 0;
+      bool go = true;
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        for (int i = 0; i < row_tiles; ++i) {
-          if (i == 0) wait(&sm.v_full[j & 1], (j / 2) & 1, &sm.dead, a.status);
-          wait(&sm.p_full[i], j & 1, &sm.dead, a.status);
+      while (go) {
+        const int row_tiles = w.rows() > 128 ? 2 : 1, n = w.t1 - w.t0;
+        wait(&sm.k_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
+        wait(&sm.q_full[0], it0++ & 1, &sm.dead, a.status);
+        tc_fence_after();
+        qk(0, jt);
+        if (row_tiles == 2) {
+          wait(&sm.q_full[1], it1++ & 1, &sm.dead, a.status);
           tc_fence_after();
-          pv(i, j);
-          if (i == row_tiles - 1) mma_commit(&sm.v_empty[j & 1]);
-          if (j + 1 < n) {
-            if (i == 0) {
-              wait(&sm.k_full[(j + 1) & 1], ((j + 1) / 2) & 1, &sm.dead, a.status);
-              tc_fence_after();
-            }
-            qk(i, j + 1);
-            if (i == row_tiles - 1) mma_commit(&sm.k_empty[(j + 1) & 1]);
-          }
+          qk(1, jt);
         }
+        mma_commit(&sm.k_empty[jt & 1]);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++jt) {
+          const bool more = j + 1 < n;
+          wait(&sm.v_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
+          wait(&sm.p_full[0], jn0++ & 1, &sm.dead, a.status);
+          tc_fence_after();
+          pv(0, jt, j > 0);
+          if (more) {
+            wait(&sm.k_full[(jt + 1) & 1], ((jt + 1) / 2) & 1, &sm.dead, a.status);
+            tc_fence_after();
+            qk(0, jt + 1);
+          }
+          if (row_tiles == 2) {
+            wait(&sm.p_full[1], jn1++ & 1, &sm.dead, a.status);
+            tc_fence_after();
+            pv(1, jt, j > 0);
+            if (more) qk(1, jt + 1);
+          }
+          mma_commit(&sm.v_empty[jt & 1]);
+          if (more) mma_commit(&sm.k_empty[(jt + 1) & 1]);
+        }
+        go = w.more();
+        if (go) w.next(a);
       }
     }
   }
@@ -578,6 +793,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   }
 }
 
+// Joins the parts of the item that starts in part blockIdx.x and ends later.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv4_tile_join_kernel(const Kv4AttnArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const Desc x = reinterpret_cast<const Desc *>(a.work_tile)[blockIdx.x];
+  if (x.seq < 0) return;
+  const float *slots = a.work_tile + gridDim.x * (sizeof(Desc) / 4);
+  const Rows q = load_rows(a, x.seq);
+  const int c0 = blockIdx.x, rows = min(kRows, q.rows - x.block * kRows);
+  auto part = [&](int c) { return slots + (2 * static_cast<size_t>(c) + (c == c0)) * slot_floats(D); };
+  const int r = blockIdx.y * (1024 / D) + threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
+  if (r >= rows) return;
+  float mx = kNegBig, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= x.last; ++c) mx = fmaxf(mx, part(c)[kRows * D + r]);
+#pragma unroll 4
+  for (int c = c0; c <= x.last; ++c) {
+    const float *p = part(c);
+    const float f = ex2f(p[kRows * D + r] - mx);
+    const float4 v = *reinterpret_cast<const float4 *>(p + r * D + d);
+    sum = fmaf(f, p[kRows * D + kRows + r], sum);
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int rr = x.block * kRows + r, qi = rr / a.group;
+  T *op = static_cast<T *>(a.out) + (q.row0 + static_cast<int64_t>(qi)) * a.o_row +
+          (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head + d;
+  using X = Kv4Type<T>;
+  uint2 o;
+  o.x = kv4_bits<uint32_t>(X::from2(acc.x * inv, acc.y * inv));
+  o.y = kv4_bits<uint32_t>(X::from2(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2 *>(op) = o;
+}
+
 template <typename T, int D>
 cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   auto kernel = kv4_tile_kernel<T, D>;
@@ -585,9 +839,8 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = ensure_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  const int64_t v = static_cast<int64_t>(a.b.rows) * a.group / kRows + a.b.n_seqs;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.c.n_kv, static_cast<unsigned>(v), 1);
+  cfg.gridDim = dim3(a.num_sms, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -596,10 +849,19 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.num_sms, kRows * D / 1024, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv4_tile_join_kernel<T, D>, a);
 }
 
 }  // namespace
+
+size_t kv4_tile_workspace(int d, int num_sms) {
+  return num_sms * sizeof(Desc) + num_sms * 2 * slot_floats(d) * sizeof(float);
+}
 
 cudaError_t launch_kv4_tile(const Kv4AttnArgs &a, cudaStream_t stream) {
   if (a.c.bf16)

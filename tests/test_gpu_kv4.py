@@ -314,6 +314,13 @@ def test_windows(window, sinks, new):
     attend(14, [20, 40, 333], new, 4, 2, 128, 32, BF16, window, sinks)
 
 
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 2, 3), (5, 2 ** 31 - 1)])
+def test_largest_windows_and_rows_before_the_start(window, sinks):
+    attend(14, [150, 6, 40], None, 8, 2, 64, 16, F16, window, sinks)
+    attend(14, [150, 6, 40], [3, 11, 2], 4, 2, 128, 16, BF16, window, sinks)
+    attend(14, [150, 6], [70, 40], 4, 2, 128, 16, F16, window, sinks)
+
+
 def test_sinks_without_a_window_change_nothing():
     a, _ = attend(15, [150, 64], None, 8, 2, 64, 16, F16)
     b, _ = attend(15, [150, 64], None, 8, 2, 64, 16, F16, sinks=9)

@@ -97,9 +97,12 @@ def test_page_bytes(lib):
 
 
 def test_workspace_size(lib):
-    assert lib.mixq_kv4_attention_workspace_size(96, 148) == 0
-    a, b = (lib.mixq_kv4_attention_workspace_size(d, 148) for d in (64, 128))
-    assert 0 < a < b and b % 16 == 0
+    size = lib.mixq_kv4_attention_workspace_size
+    assert size(96, 1, 148) == 0 and size(128, -1, 148) == 0
+    for d in (64, 128):
+        assert 0 < size(d, 1, 148) == size(d, 32, 148) < size(d, 33, 148) == size(d, 0, 148)
+        assert size(d, 1, 148) % 16 == 0
+    assert size(64, 1, 148) < size(128, 1, 148)
 
 
 def _desc(**kw):
