@@ -38,7 +38,7 @@
 namespace mixq {
 namespace {
 
-constexpr int kThreads = 640;  // 8 softmax, 8 unpack, 1 MMA warp (and 3 that complete its group)
+constexpr int kThreads = 896;  // softmax 0-7, K 8-15, V 16-23, MMA 24, walk 25 (26, 27 complete its group)
 constexpr int kRows = 256;     // query rows per CTA
 constexpr int kKeys = 128;     // keys per tile
 constexpr int kSeqChunk = 64;  // sequences the search for a CTA's part looks at together
@@ -46,9 +46,18 @@ constexpr int kMinTiles = 4;   // key tiles per part: below, joining costs more 
 constexpr float kNegBig = -1e30f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// registers per thread after the split; 256*128 + 256*80 + 128*64 = 61440, the
-// 640 * 96 the CTA starts with
-constexpr int kRegsSoftmax = 128, kRegsUnpack = 80, kRegsMma = 64;
+constexpr int kItems = 8;      // items the walk may be ahead
+
+// registers per thread after the split; 256*144 + 512*40 + 128*56 = 64512, the 896 * 72 the CTA
+// starts with
+constexpr int kRegsSoftmax = 144, kRegsUnpack = 40, kRegsMma = 56;
+
+// A part of an item: key tiles [t0, t0 + n) of a block of rows.  n == 0: no more.
+struct Item {
+  int n, t0, tiles, sinks, skip;  // tiles of the whole item; tile i is key tile i, from sinks on i + skip
+  int row0, rows, len, pos0;      // rows: of this block
+  int first, head;                // first row of the block within the sequence's rows
+};
 
 template <int D>
 struct TileSmem {
@@ -57,7 +66,10 @@ struct TileSmem {
   alignas(1024) uint8_t v[2][kKeys * D * 2];
   alignas(16) float4 kp[4][kKeys / 2];  // per pair of keys: s0 s1 lo0 lo1, times scale log2(e)
   alignas(8) uint8_t hidden[4][8];  // records of the tile whose page is not usable
+  Item item[kItems];
+  int64_t src[2][32];  // records of four tiles: offset in the pages, -1 beyond the keys, -2 page not usable
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], par_full[4], s_full[2], p_full[2], o_full[2];
+  uint64_t item_full[kItems], item_empty[kItems], src_full[2], src_empty[2], done;
   long long cost[kSeqChunk];
   int found;
   long long found_start;
@@ -233,7 +245,6 @@ struct Walk {
   int left;    // tiles of the part from t0 on
 
   __device__ __forceinline__ void set() { t1 = min(k.tiles, t0 + left); }
-  __device__ __forceinline__ bool more() const { return left > t1 - t0; }
   __device__ __forceinline__ void next(const Kv4AttnArgs &a) {
     left -= t1 - t0;
     t0 = 0;
@@ -271,8 +282,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 
   if (tid == 0) {
     sm.dead = 0;
+    mbar_init(&sm.done, 1);
+    for (int i = 0; i < kItems; ++i) {
+      sm.item[i].n = 0;
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], 9);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.q_full[i], 128);
+      mbar_init(&sm.src_full[i], 1);
+      mbar_init(&sm.src_empty[i], 16);
+      mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.k_full[i], 8);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], 8);
@@ -284,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     for (int i = 0; i < 4; ++i) mbar_init(&sm.par_full[i], 8);
     fence_mbar_init();
   }
-  if (warp == 16) {
+  if (tid < 64) sm.src[tid / 32][tid % 32] = -1;
+  if (warp == 24) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
@@ -308,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   const int mylen = static_cast<int>(min(quota, total - lo));
   Desc *desc = reinterpret_cast<Desc *>(a.work_tile);
   float *slots = a.work_tile + gridDim.x * (sizeof(Desc) / 4);
-  if (tid == 0) desc[blockIdx.x].seq = -1;
   Walk w{};
   if (mylen > 0) {
     long long base = 0;
@@ -374,58 +393,73 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     reg_inc<kRegsSoftmax>();
     const int i = warp / 4, row = tid & 127, r = i * 128 + row;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes per warp
-    int jt = 0;              // key tiles of the CTA so far
-    int jn = 0;              // those of this row tile (its barriers' phases)
+    int jt = 0;  // key tiles of the CTA so far
+    int jn = 0;  // those of this row tile (its barriers' phases)
     float qsum = 0.f;
-    // the thread's query row into the operand tile, and its sum
-    auto load_q = [&]() {
-      if (i * 128 >= w.rows()) return;
-      const int rr = w.block * kRows + r, qi = rr / a.group;
-      const bool valid = r < w.rows();
-      const T *qp = static_cast<const T *>(a.q) + (w.q.row0 + static_cast<int64_t>(qi)) * a.q_row +
-                    (static_cast<int64_t>(w.head) * a.group + (rr - qi * a.group)) * a.q_head;
-      qsum = 0.f;
+    // The warp's 32 query rows of an item into the operand tile, D/8 lanes a row; then, once they
+    // are there, each lane's sum over its own row.
+    auto fetch_q = [&](const Item &x) {
+      if (i * 128 >= x.rows) return;
+      const int rr = x.first + r, qi = rr / a.group;
+      const int64_t at = (x.row0 + static_cast<int64_t>(qi)) * a.q_row +
+                         (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.q_head;
+      constexpr int LANES = D / 8, RPW = 32 / LANES;
+      const int l = lane % LANES;
+#pragma unroll 4
+      for (int y = 0; y < 32; y += RPW) {
+        const int z = y + lane / LANES, tr = (warp & 3) * 32 + z;
+        const int64_t from = __shfl_sync(0xffffffffu, at, z);
+        const bool valid = i * 128 + tr < x.rows;
+        cp_async16(smem_u32(sm.q[i]) + (l / 8) * 16384 + tr * 128 + (((l & 7) ^ (tr & 7)) << 4),
+                   static_cast<const T *>(a.q) + (valid ? from : 0) + l * 8, valid ? 16 : 0);
+      }
+    };
+    auto have_q = [&](const Item &x) {
+      if (i * 128 >= x.rows) return;
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full[i]);
+      uint64_t sum = 0;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c) : make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        const uint4 x4 = *reinterpret_cast<const uint4 *>(sm.q[i] + (c / 8) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        const uint32_t u[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = X::f2(kv4_bits<T2>(u[e]));
-          qsum += f.x;
-          qsum += f.y;
+          sum = add2(sum, pack2(f.x, f.y));
         }
-        *reinterpret_cast<uint4 *>(sm.q[i] + (c / 8) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x;
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.q_full[i]);
+      const float2 f = unpack2(sum);
+      qsum = f.x + f.y;
     };
-    if (mylen > 0) load_q();
-    bool go = mylen > 0;
+    wait(&sm.item_full[0], 0, &sm.dead, a.status);
+    if (sm.item[0].n > 0) {
+      fetch_q(sm.item[0]);
+      have_q(sm.item[0]);
+    }
 #pragma unroll 1
-    while (go) {
-      const int rows = w.rows(), first = w.block * kRows, n = w.t1 - w.t0;
-      const bool active = i * 128 < rows, valid = r < rows;
-      const int qi = (first + r) / a.group;
-      const int64_t head_q = static_cast<int64_t>(w.head) * a.group + (first + r - qi * a.group);
-      const int64_t orow = w.q.row0 + static_cast<int64_t>(qi);
-      // key j is visible when j < vis and (j >= wlo or j < sinks)
-      const int vis = valid ? min(w.q.pos0 + qi + 1, w.q.len) : w.q.len;
-      const int wlo = valid && a.window > 0 ? max(max(w.q.pos0 + qi, 0) - a.window + 1, 0) : 0;
-      const int tmin = min(w.q.pos0 + (first + i * 128) / a.group + 1, w.q.len);
-      const int tmax = max(w.q.pos0 + (first + min(i * 128 + 128, rows) - 1) / a.group, 0);
-      const Keys keys = w.k;
-      const int t0 = w.t0;
-      const bool begins = w.t0 == 0, ends = w.t1 == w.k.tiles;
-      float base = 0.f;            // what is added to t: 6 - m once a key was seen
-      float limit = -INFINITY;     // t + base above this moves the maximum
+    for (int it = 0;; ++it) {
+      const Item &x = sm.item[it % kItems], &nx = sm.item[(it + 1) % kItems];  // x has arrived already
+      const int n = x.n;
+      if (n == 0 || sm.dead) break;
+      const bool active = i * 128 < x.rows;
       uint64_t la = pack2(0.f, 0.f), lb = la;
-      const uint64_t qs2 = pack2(qsum, qsum);
-
+      float base = 0.f;         // what is added to t: 6 - m once a key was seen
+      float limit = -INFINITY;  // t + base above this moves the maximum
       if (active) {
+        const bool valid = r < x.rows;
+        const int qi = (x.first + r) / a.group, t0 = x.t0, sinks = x.sinks, skip = x.skip;
+        // key j is visible when j < vis and (j >= wlo or j < sinks)
+        const int vis = valid ? min(x.pos0 + qi + 1, x.len) : x.len;
+        const int wlo = valid && a.window > 0 ? max(max(x.pos0 + qi, 0) - a.window + 1, 0) : 0;
+        const int tmin = min(x.pos0 + (x.first + i * 128) / a.group + 1, x.len);
+        const int tmax = max(x.pos0 + (x.first + min(i * 128 + 128, x.rows) - 1) / a.group, 0);
+        const uint64_t qs2 = pack2(qsum, qsum);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          const int k0 = keys.key0(t0 + j), st = (jt + j) & 3;
+          const int k0 = (t0 + j + (t0 + j >= sinks ? skip : 0)) * kKeys, st = (jt + j) & 3;
           wait(&sm.par_full[st], ((jt + j) >> 2) & 1, &sm.dead, a.status);
           const float4 *kp = sm.kp[st];
           const uint2 hid = *reinterpret_cast<const uint2 *>(sm.hidden[st]);
@@ -433,6 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
                              (a.window <= 0 || k0 > tmax - a.window || k0 + kKeys <= a.sinks);
           wait(&sm.s_full[i], (jn + j) & 1, &sm.dead, a.status);
           tc_fence_after();
+          if (j + 1 == n) {  // the last scores are there, so the operand tile is free for the next rows
+            wait(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
+            if (nx.n > 0) fetch_q(nx);
+          }
           union Chunk {
             uint32_t u[32];
             float f[32];
@@ -512,23 +550,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           tmem_ld_wait();
           tmem_ld32(tm_s[i] + lanes + 32, buf[1].u);
           float mx = scores(buf[0], 0);
+          // not unrolled further: the roles share the instruction cache
+#pragma unroll 1
+          for (int c0 = 0; c0 < 4; c0 += 2) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            Chunk &t = buf[c & 1];
-            if (__any_sync(0xffffffffu, mx > limit)) grow(t, c, mx);
-            if (c < 3) tmem_ld_wait();
-            uint32_t p[16];
+            for (int h = 0; h < 2; ++h) {
+              const int c = c0 + h;
+              const bool next = h == 0 || c0 == 0;
+              Chunk &t = buf[h];
+              if (__any_sync(0xffffffffu, mx > limit)) grow(t, c, mx);
+              if (next) tmem_ld_wait();
+              uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = unpack2(t.d[e]);
-              const float p0 = ex2f(x.x), p1 = ex2f(x.y);
-              if (e & 1) lb = add2(lb, pack2(p0, p1));
-              else la = add2(la, pack2(p0, p1));
-              p[e] = kv4_bits<uint32_t>(X::from2(p0, p1));
+              for (int e = 0; e < 16; ++e) {
+                const float2 x = unpack2(t.d[e]);
+                const float p0 = ex2f(x.x), p1 = ex2f(x.y);
+                if (e & 1) lb = add2(lb, pack2(p0, p1));
+                else la = add2(la, pack2(p0, p1));
+                p[e] = kv4_bits<uint32_t>(X::from2(p0, p1));
+              }
+              if (next) mx = scores(buf[h ^ 1], c + 1);
+              tmem_st16(tm_s[i] + lanes + c * 16, p);
+              if (c0 == 0) tmem_ld32(tm_s[i] + lanes + (c + 2) * 32, t.u);
             }
-            if (c < 3) mx = scores(buf[(c + 1) & 1], c + 1);
-            tmem_st16(tm_s[i] + lanes + c * 16, p);
-            if (c < 2) tmem_ld32(tm_s[i] + lanes + (c + 2) * 32, t.u);
           }
           tmem_st_wait();
           tc_fence_before();
@@ -536,27 +580,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           if (lane == 0) mbar_arrive(&sm.p_full[i]);
         }
         jn += n;
+      } else {
+        wait(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
+        if (nx.n > 0) fetch_q(nx);
       }
       jt += n;
-      // ---- on to the next item's queries, then this one's result.  Column c of O is dim 2c,
-      // column D/2 + c dim 2c + 1.
-      go = w.more();
-      if (go) {
-        w.next(a);
-        load_q();
-      } else if (warp == 0 && lane == 0 && begins && !ends) {
-        const long long end = lo + mylen + (keys.tiles - (t0 + n));
-        desc[blockIdx.x] = Desc{w.seq, w.block, w.head, static_cast<int>((end - 1) / quota)};
-      }
+      if (nx.n > 0) have_q(nx);
+      // ---- the result.  Column c of O is dim 2c, column D/2 + c dim 2c + 1.
       if (active) {
         const float2 l0 = unpack2(la), l1 = unpack2(lb);
         const float sum = (l0.x + l0.y) + (l1.x + l1.y);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const bool valid = r < x.rows, begins = x.t0 == 0, full = begins && x.t0 + n == x.tiles;
+        const int rr = x.first + r, qi = rr / a.group;
+        T *op = static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
+                (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head;
+        float *part = slots + (2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0)) * slot_floats(D);
         wait(&sm.o_full[i], (jn - 1) & 1, &sm.dead, a.status);
         tc_fence_after();
-        const bool full = begins && ends;
-        float *part = slots + (2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0)) * slot_floats(D);
-        T *op = static_cast<T *>(a.out) + orow * a.o_row + head_q * a.o_head;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t e0[16], e1[16];
@@ -566,11 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           if (valid && full) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              uint32_t x[4];
+              uint32_t y[4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                x[y] = kv4_bits<uint32_t>(X::from2(__uint_as_float(e0[4 * e + y]) * inv, __uint_as_float(e1[4 * e + y]) * inv));
-              reinterpret_cast<uint4 *>(op)[c * 4 + e] = make_uint4(x[0], x[1], x[2], x[3]);
+              for (int z = 0; z < 4; ++z)
+                y[z] = kv4_bits<uint32_t>(X::from2(__uint_as_float(e0[4 * e + z]) * inv, __uint_as_float(e1[4 * e + z]) * inv));
+              reinterpret_cast<uint4 *>(op)[c * 4 + e] = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else if (valid) {
 #pragma unroll
@@ -584,114 +625,109 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         }
         tc_fence_before();
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[it % kItems]);
     }
-  } else if (warp < 16) {
+  } else if (warp < 24) {
     // -------------------------------------------------------------- unpack
+    // One record a warp and tile: its K codes and pairs (warps 8-15), its V rows (16-23).
     reg_dec<kRegsUnpack>();
-    const int rw = warp - 8, g = lane >> 2, t = lane & 3;
-    const float sl2 = a.scale * 1.4426950408889634f;
-    uint4 k[2], v[D / 64];
-    uint32_t pr = 0;  // lane's (s, lo): token lane % 16, of K below lane 16 and V above
-    int state = 0;    // of the loaded record: 0 beyond the keys, 1 loaded, 2 page not usable
-    // two steps ahead of the unpacking: the page of a record, one turn later its bytes
-    int pj = 0;        // next tile of w whose page is asked for
-    int page = -1;     // -1: beyond the keys
-    int64_t off = 0;   // of the record in its page
-    bool any = mylen > 0;
-    auto ask = [&]() {
-      page = -1;
-      off = -1;
-      if (!any) return;
-      if (pj == w.t1 - w.t0) {
-        any = w.more();
-        if (!any) return;
-        w.next(a);
-        pj = 0;
+    const int rw = warp & 7, g = lane >> 2, t = lane & 3;
+    const bool for_k = warp < 16;
+    uint4 x[D / 64];
+    uint32_t pr = 0;    // lane's (s, lo): token lane % 16, of K below lane 16 and V above
+    bool gone = false;  // the record's page is not usable
+    auto load = [&](int j) {
+      if (j >= mylen) return;
+      const int b = j >> 2;
+      if ((j & 3) == 0) wait(&sm.src_full[b & 1], b >> 1 & 1, &sm.dead, a.status);
+      const int64_t off = sm.src[b & 1][(j & 3) * 8 + rw];
+      if ((j & 3) == 3) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.src_empty[b & 1]);
       }
-      const int key = w.k.key0(w.t0 + pj) + rw * 16;
-      ++pj;
-      if (key >= w.q.len) return;
-      const int rec = key / 16;
-      const int slot = a.c.page_shift >= 0 ? rec >> a.c.page_shift : rec / a.c.recs_per_page;
-      page = __ldg(a.b.table + w.seq * a.b.table_stride + slot);
-      off = (static_cast<int64_t>(w.head) * a.c.recs_per_page + (rec - slot * a.c.recs_per_page)) * REC;
-    };
-    auto load = [&]() {
-      k[0] = k[1] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) v[c] = make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < D / 64; ++c) x[c] = make_uint4(0, 0, 0, 0);
       pr = 0;
-      state = off < 0 ? 0 : page < 0 || page >= a.c.n_pages ? 2 : 1;
-      if (state == 2 && lane == 0) record_error(a.status, kErrInvalidArg);
-      if (state != 1) return;
-      const uint8_t *rec = a.c.pages + page * a.c.page_stride + off;
-      if (D == 128) {
-        k[0] = __ldg(reinterpret_cast<const uint4 *>(rec) + lane);
-        k[1] = __ldg(reinterpret_cast<const uint4 *>(rec + 512) + lane);
-      } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(rec) + lane);
-        const uint2 y = __ldg(reinterpret_cast<const uint2 *>(rec + 256) + lane);
-        k[0] = make_uint4(x.x, x.y, y.x, y.y);
-      }
+      gone = off == -2;
+      if (off < 0) return;
+      const uint8_t *rec = a.c.pages + off;
+      if (!for_k) {
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) v[c] = __ldg(reinterpret_cast<const uint4 *>(rec + 8 * D + c * 512) + lane);
+        for (int c = 0; c < D / 64; ++c) x[c] = __ldg(reinterpret_cast<const uint4 *>(rec + 8 * D + c * 512) + lane);
+      } else if (D == 128) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) x[c] = __ldg(reinterpret_cast<const uint4 *>(rec + c * 512) + lane);
+      } else {
+        const uint2 y = __ldg(reinterpret_cast<const uint2 *>(rec) + lane), z = __ldg(reinterpret_cast<const uint2 *>(rec + 256) + lane);
+        x[0] = make_uint4(y.x, y.y, z.x, z.y);
+      }
       pr = __ldg(reinterpret_cast<const uint32_t *>(rec + 16 * D) + lane);
     };
-    ask();
-    load();
-    ask();
-#pragma unroll 1
-    for (int j = 0; j < mylen; ++j) {
-      const int st = j & 1;
-      // pairs: a row whose own K or V pair is not finite scores NaN and has V = 0, so that
-      // only queries that see it become NaN
-      const float2 own = kv4_pair<BF>(pr);
+    // A row whose own K or V pair is not finite scores NaN and has V = 0, so that only queries
+    // that see it become NaN.
+    auto finite = [&](float2 own) -> bool {
       const bool fin = (own.x + own.y) - (own.x + own.y) == 0.f;
-      const bool both = __shfl_xor_sync(0xffffffffu, static_cast<int>(fin), 16) && fin;
-      if (j >= 2) wait(&sm.k_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
-      if (lane < 16) {
-        float *kp = reinterpret_cast<float *>(&sm.kp[j & 3][rw * 8 + lane / 2]) + (lane & 1);
-        kp[0] = both ? own.x * sl2 : 0.f;
-        kp[2] = both ? own.y * sl2 : NAN;
-      }
-      if (lane == 0) sm.hidden[j & 3][rw] = state == 2;
-      // ---- K codes: lane (g, t) has dims [t D/4, (t+1) D/4) of keys g and g + 8
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint8_t *kt = sm.k[st] + (rw * 16 + h * 8 + g) * 128;
-        uint32_t word[WORDS];
-        if (D == 128) {
-          // lanes t >= 2 take their words in another order: eight lanes of a 16-byte store then
-          // hit eight different 16-byte banks
-          const bool swap = t & 2;
-          word[0] = swap ? k[h].z : k[h].x, word[1] = swap ? k[h].w : k[h].y;
-          word[WORDS - 2] = swap ? k[h].x : k[h].z, word[WORDS - 1] = swap ? k[h].y : k[h].w;
-        } else {
-          word[0] = h ? k[0].z : k[0].x, word[1] = h ? k[0].w : k[0].y;
+      return __shfl_xor_sync(0xffffffffu, static_cast<int>(fin), 16) && fin;
+    };
+    load(0);
+    if (for_k) {
+      const float sl2 = a.scale * 1.4426950408889634f;
+#pragma unroll 1
+      for (int j = 0; j < mylen; ++j) {
+        const int st = j & 1;
+        const float2 own = kv4_pair<BF>(pr);
+        const bool both = finite(own);
+        if (j >= 2) wait(&sm.k_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
+        if (lane < 16) {
+          float *kp = reinterpret_cast<float *>(&sm.kp[j & 3][rw * 8 + lane / 2]) + (lane & 1);
+          kp[0] = both ? own.x * sl2 : 0.f;
+          kp[2] = both ? own.y * sl2 : NAN;
         }
-#pragma unroll
-        for (int x = 0; x < WORDS; ++x) {
-          T2 c[4];
-          Codes<T>::pairs(word[x], c);
-          const int chunk = t * WORDS + (D == 128 ? x ^ (t & 2) : x);  // 16-byte chunk of the row: 8 dims
-          *reinterpret_cast<uint4 *>(kt + (chunk / 8) * 16384 + (((chunk & 7) ^ g) << 4)) =
-              make_uint4(kv4_bits<uint32_t>(c[0]), kv4_bits<uint32_t>(c[1]), kv4_bits<uint32_t>(c[2]),
-                         kv4_bits<uint32_t>(c[3]));
+        if (lane == 0) sm.hidden[j & 3][rw] = gone;
+        // ---- K codes: lane (g, t) has dims [t D/4, (t+1) D/4) of keys g and g + 8
+  #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint8_t *kt = sm.k[st] + (rw * 16 + h * 8 + g) * 128;
+          uint32_t word[WORDS];
+          if constexpr (D == 128) {
+            // lanes t >= 2 take their words in another order: eight lanes of a 16-byte store then
+            // hit eight different 16-byte banks
+            const bool swap = t & 2;
+            word[0] = swap ? x[h].z : x[h].x, word[1] = swap ? x[h].w : x[h].y;
+            word[WORDS - 2] = swap ? x[h].x : x[h].z, word[WORDS - 1] = swap ? x[h].y : x[h].w;
+          } else {
+            word[0] = h ? x[0].z : x[0].x, word[1] = h ? x[0].w : x[0].y;
+          }
+  #pragma unroll
+          for (int y = 0; y < WORDS; ++y) {
+            T2 c[4];
+            Codes<T>::pairs(word[y], c);
+            const int chunk = t * WORDS + (D == 128 ? y ^ (t & 2) : y);  // 16-byte chunk of the row: 8 dims
+            *reinterpret_cast<uint4 *>(kt + (chunk / 8) * 16384 + (((chunk & 7) ^ g) << 4)) =
+                make_uint4(kv4_bits<uint32_t>(c[0]), kv4_bits<uint32_t>(c[1]), kv4_bits<uint32_t>(c[2]),
+                           kv4_bits<uint32_t>(c[3]));
+          }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.k_full[st]);
+          mbar_arrive(&sm.par_full[j & 3]);
+        }
+        load(j + 1);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.k_full[st]);
-        mbar_arrive(&sm.par_full[j & 3]);
-      }
-      // ---- V rows, transposed: tile row = dim (2b at b, 2b + 1 at D/2 + b), 64 keys per 128-byte atom
-      if (j >= 2) wait(&sm.v_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
-      {
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < mylen; ++j) {
+        const int st = j & 1;
+        const bool both = finite(kv4_pair<BF>(pr));
+        if (j >= 2) wait(&sm.v_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
+        // transposed: tile row = dim (2b at b, 2b + 1 at D/2 + b), 64 keys per 128-byte atom
         // (s, lo) of this lane's tokens 2t, 2t+1 and 2t+8, 2t+9 in the type
         const uint32_t use = both ? pr : 0u;
         uint32_t q[4];
-#pragma unroll
+  #pragma unroll
         for (int e = 0; e < 4; ++e) q[e] = __shfl_sync(0xffffffffu, use, 16 + 2 * t + (e & 1) + 8 * (e >> 1));
         const T2 s0 = kv4_bits<T2>(__byte_perm(q[0], q[1], 0x5410)), l0 = kv4_bits<T2>(__byte_perm(q[0], q[1], 0x7632));
         const T2 s1 = kv4_bits<T2>(__byte_perm(q[2], q[3], 0x5410)), l1 = kv4_bits<T2>(__byte_perm(q[2], q[3], 0x7632));
@@ -699,13 +735,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         const int c0 = (rw & 3) * 2;  // chunk of tokens 0..7 of the record
         uint8_t *v0 = sm.v[st] + (rw / 4) * (D * 128) + g * 128 + 4 * t + ((c0 ^ g) << 4);
         uint8_t *v1 = sm.v[st] + (rw / 4) * (D * 128) + g * 128 + 4 * t + (((c0 + 1) ^ g) << 4);
-#pragma unroll
+  #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
+          const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+  #pragma unroll
           for (int e = 0; e < 4; ++e) {
             T2 o[4];  // (dim 2b, tokens 2t..), (2b + 1, 2t..), (2b, 2t+8..), (2b + 1, 2t+8..)
-            Codes<T>::pairs(x[e], o);
+            Codes<T>::pairs(y[e], o);
             const int at = (c * 32 + e * 8) * 128;
             // 15 s + lo can pass the type's largest value (s is rounded): hold it there
             *reinterpret_cast<T2 *>(v0 + at) = __hmin2(__hfma2(o[0], s0, l0), top);
@@ -714,17 +750,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             *reinterpret_cast<T2 *>(v1 + at + D * 64) = __hmin2(__hfma2(o[3], s1, l1), top);
           }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_full[st]);
+        load(j + 1);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[st]);
-      load();
-      ask();
     }
   } else {
-    // ----------------------------------------------------------------- MMA
     reg_dec<kRegsMma>();
-    if (warp == 16 && lane == 0 && mylen > 0) {
+    if (warp == 24 && lane == 0) {
+      // --------------------------------------------------------------- MMA
       constexpr uint32_t kind = BF ? (1u << 7) | (1u << 10) : 0u;
       constexpr uint32_t id_qk = idesc_f16_f32(128, kKeys) | kind, id_pv = idesc_f16_f32(128, D) | kind;
       auto qk = [&](int i, int jt) {
@@ -745,49 +780,114 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         }
         mma_commit(&sm.o_full[i]);
       };
-      int jt = 0, jn0 = 0, jn1 = 0, it0 = 0, it1 = 0;
-      bool go = true;
+      // Per key tile and row tile: O += P V, then S of the next key tile, which may be the next item's.
+      int it = 0, j = 0, n = 0, row_tiles = 0;  // of the tile whose P V comes next
+      uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
 #pragma unroll 1
-      while (go) {
-        const int row_tiles = w.rows() > 128 ? 2 : 1, n = w.t1 - w.t0;
-        wait(&sm.k_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
-        wait(&sm.q_full[0], it0++ & 1, &sm.dead, a.status);
-        tc_fence_after();
-        qk(0, jt);
-        if (row_tiles == 2) {
-          wait(&sm.q_full[1], it1++ & 1, &sm.dead, a.status);
-          tc_fence_after();
-          qk(1, jt);
+      for (int jt = -1;; ++jt) {
+        int next_n = n, next_tiles = row_tiles;
+        const bool turn = j + 1 >= n;  // the next scores are another item's
+        if (turn) {
+          const int slot = (n ? it + 1 : it) % kItems;
+          wait(&sm.item_full[slot], (n ? it + 1 : it) / kItems & 1, &sm.dead, a.status);
+          next_n = sm.item[slot].n;
+          next_tiles = next_n == 0 || sm.dead ? 0 : sm.item[slot].rows > 128 ? 2 : 1;
+          mbar_arrive(&sm.item_empty[slot]);
         }
-        mma_commit(&sm.k_empty[jt & 1]);
-#pragma unroll 1
-        for (int j = 0; j < n; ++j, ++jt) {
-          const bool more = j + 1 < n;
-          wait(&sm.v_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
-          wait(&sm.p_full[0], jn0++ & 1, &sm.dead, a.status);
-          tc_fence_after();
-          pv(0, jt, j > 0);
-          if (more) {
-            wait(&sm.k_full[(jt + 1) & 1], ((jt + 1) / 2) & 1, &sm.dead, a.status);
+        if (row_tiles) wait(&sm.v_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i < row_tiles) {
+            wait(&sm.p_full[i], p_phase[i], &sm.dead, a.status);
+            p_phase[i] ^= 1;
             tc_fence_after();
-            qk(0, jt + 1);
+            pv(i, jt, j > 0);
           }
-          if (row_tiles == 2) {
-            wait(&sm.p_full[1], jn1++ & 1, &sm.dead, a.status);
+          if (i < next_tiles) {
+            if (i == 0) wait(&sm.k_full[(jt + 1) & 1], ((jt + 1) / 2) & 1, &sm.dead, a.status);
+            if (turn) {
+              wait(&sm.q_full[i], q_phase[i], &sm.dead, a.status);
+              q_phase[i] ^= 1;
+            }
             tc_fence_after();
-            pv(1, jt, j > 0);
-            if (more) qk(1, jt + 1);
+            qk(i, jt + 1);
           }
-          mma_commit(&sm.v_empty[jt & 1]);
-          if (more) mma_commit(&sm.k_empty[(jt + 1) & 1]);
         }
-        go = w.more();
-        if (go) w.next(a);
+        if (row_tiles) mma_commit(&sm.v_empty[jt & 1]);
+        if (!next_tiles) break;
+        mma_commit(&sm.k_empty[(jt + 1) & 1]);
+        if (turn) {
+          if (n) ++it;
+          j = 0;
+        } else {
+          ++j;
+        }
+        n = next_n;
+        row_tiles = next_tiles;
       }
+      mma_commit(&sm.done);  // nothing in flight when the CTA gives its memory back
+      mbar_wait(&sm.done, 0, kWaitNs);
+    } else if (warp == 25) {
+      // -------------------------------------------------------------- walk
+      // Items and the places of records, four tiles (32 lanes) at a time, ahead of the other roles.
+      int it = 0, pj = 0;
+      auto publish = [&](bool end) {
+        if (it >= kItems) wait(&sm.item_empty[it % kItems], (it / kItems - 1) & 1, &sm.dead, a.status);
+        if (lane == 0)
+          sm.item[it % kItems] = Item{end ? 0 : w.t1 - w.t0, w.t0, w.k.tiles, w.k.sinks, w.k.skip, w.q.row0, w.rows(),
+                                      w.q.len, w.q.pos0, w.block * kRows, w.head};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_full[it % kItems]);
+        ++it;
+      };
+      Desc d{-1, 0, 0, 0};
+      if (mylen > 0) {
+        publish(false);
+#pragma unroll 1
+        for (int b = 0; b * 4 < mylen; ++b) {
+          int key = 0, len = 0, seq = 0, head = 0;
+#pragma unroll 1
+          for (int x = 0; x < 4 && b * 4 + x < mylen; ++x, ++pj) {
+            if (pj == w.t1 - w.t0) {
+              w.next(a);
+              pj = 0;
+              publish(false);
+            }
+            if (lane / 8 == x) {
+              key = w.k.key0(w.t0 + pj) + (lane & 7) * 16;
+              len = w.q.len;
+              seq = w.seq;
+              head = w.head;
+            }
+          }
+          int64_t off = -1;
+          if (key < len) {
+            const int rec = key / 16;
+            const int slot = a.c.page_shift >= 0 ? rec >> a.c.page_shift : rec / a.c.recs_per_page;
+            const int page = __ldg(a.b.table + seq * a.b.table_stride + slot);
+            if (page < 0 || page >= a.c.n_pages) {
+              off = -2;
+              record_error(a.status, kErrInvalidArg);
+            } else {
+              off = page * a.c.page_stride + (static_cast<int64_t>(head) * a.c.recs_per_page + (rec - slot * a.c.recs_per_page)) * REC;
+            }
+          }
+          if (b >= 2) wait(&sm.src_empty[b & 1], (b / 2 - 1) & 1, &sm.dead, a.status);
+          sm.src[b & 1][lane] = off;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.src_full[b & 1]);
+        }
+        if (w.t0 == 0 && w.t1 < w.k.tiles) {
+          const long long end = lo + mylen + (w.k.tiles - w.t1);
+          d = Desc{w.seq, w.block, w.head, static_cast<int>((end - 1) / quota)};
+        }
+      }
+      publish(true);
+      if (lane == 0) desc[blockIdx.x] = d;
     }
   }
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 24) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -106,6 +106,17 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t *bar, uint32_t parity,
   }
 }
 
+// ------------------------------------------------------------------ cp.async
+// 16 bytes global -> shared; the bytes from `have` (0 or 16) on are zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void *src, uint32_t have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(have)
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
