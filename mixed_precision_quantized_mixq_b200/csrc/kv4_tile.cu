@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kv4.h"
 #include "ptx.cuh"
@@ -386,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 256 + D};
+  auto tm_s = [tmem](int i) { return tmem + i * 128; };
+  auto tm_o = [tmem](int i) { return tmem + 256 + i * D; };
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
               const float4 x = kp[c * 16 + e];
               t.d[e] = fma2(t.d[e], pack2(x.x, x.y), fma2(pack2(x.z, x.w), qs2, b2));
             }
-            if (!whole) {
+            if (__builtin_expect(!whole, 0)) {
               // one bit per key, so that no lane branches
               const int kc = k0 + c * 32;
               const uint32_t off = (c < 2 ? hid.x : hid.y) >> ((c & 1) * 16);
@@ -520,11 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 #pragma unroll 1
               for (int x = 0; x < D / 16; ++x) {
                 uint32_t o[16];
-                tmem_ld16(tm_o[i] + lanes + x * 16, o);
+                tmem_ld16(tm_o(i) + lanes + x * 16, o);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                tmem_st16(tm_o[i] + lanes + x * 16, o);
+                tmem_st16(tm_o(i) + lanes + x * 16, o);
               }
             }
             if (c > 0) {
@@ -532,23 +534,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 #pragma unroll 1
               for (int x = 0; x < c; ++x) {
                 uint32_t o[16];
-                tmem_ld16(tm_s[i] + lanes + x * 16, o);
+                tmem_ld16(tm_s(i) + lanes + x * 16, o);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   const float2 f = X::f2(kv4_bits<T2>(o[e]));
                   o[e] = kv4_bits<uint32_t>(X::from2(f.x * al, f.y * al));
                 }
-                tmem_st16(tm_s[i] + lanes + x * 16, o);
+                tmem_st16(tm_s(i) + lanes + x * 16, o);
               }
             }
             tmem_st_wait();
           };
           // 32 keys at a time: the exponentials of one chunk beside the scores of the next.  P of
           // keys [32c, 32c + 32) takes TMEM columns [16c, 16c + 16), whose scores have been read.
-          tmem_ld32(tm_s[i] + lanes, buf[0].u);
+          tmem_ld32(tm_s(i) + lanes, buf[0].u);
           tmem_ld_wait();
-          tmem_ld32(tm_s[i] + lanes + 32, buf[1].u);
+          tmem_ld32(tm_s(i) + lanes + 32, buf[1].u);
           float mx = scores(buf[0], 0);
           // not unrolled further: the roles share the instruction cache
 #pragma unroll 1
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
               const int c = c0 + h;
               const bool next = h == 0 || c0 == 0;
               Chunk &t = buf[h];
-              if (__any_sync(0xffffffffu, mx > limit)) grow(t, c, mx);
+              if (__builtin_expect(__any_sync(0xffffffffu, mx > limit), 0)) grow(t, c, mx);
               if (next) tmem_ld_wait();
               uint32_t p[16];
 #pragma unroll
@@ -570,8 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
                 p[e] = kv4_bits<uint32_t>(X::from2(p0, p1));
               }
               if (next) mx = scores(buf[h ^ 1], c + 1);
-              tmem_st16(tm_s[i] + lanes + c * 16, p);
-              if (c0 == 0) tmem_ld32(tm_s[i] + lanes + (c + 2) * 32, t.u);
+              tmem_st16(tm_s(i) + lanes + c * 16, p);
+              if (c0 == 0) tmem_ld32(tm_s(i) + lanes + (c + 2) * 32, t.u);
             }
           }
           tmem_st_wait();
@@ -601,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t e0[16], e1[16];
-          tmem_ld16(tm_o[i] + lanes + c * 16, e0);
-          tmem_ld16(tm_o[i] + lanes + D / 2 + c * 16, e1);
+          tmem_ld16(tm_o(i) + lanes + c * 16, e0);
+          tmem_ld16(tm_o(i) + lanes + D / 2 + c * 16, e1);
           tmem_ld_wait();
           if (valid && full) {
 #pragma unroll
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         }
         if (lane == 0) sm.hidden[j & 3][rw] = gone;
         // ---- K codes: lane (g, t) has dims [t D/4, (t+1) D/4) of keys g and g + 8
-  #pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint8_t *kt = sm.k[st] + (rw * 16 + h * 8 + g) * 128;
           uint32_t word[WORDS];
@@ -694,12 +696,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             // lanes t >= 2 take their words in another order: eight lanes of a 16-byte store then
             // hit eight different 16-byte banks
             const bool swap = t & 2;
-            word[0] = swap ? x[h].z : x[h].x, word[1] = swap ? x[h].w : x[h].y;
-            word[WORDS - 2] = swap ? x[h].x : x[h].z, word[WORDS - 1] = swap ? x[h].y : x[h].w;
+            word[0] = swap ? x[0].z : x[0].x, word[1] = swap ? x[0].w : x[0].y;
+            word[WORDS - 2] = swap ? x[0].x : x[0].z, word[WORDS - 1] = swap ? x[0].y : x[0].w;
+            x[0] = x[D / 64 - 1];  // then keys g + 8
           } else {
             word[0] = h ? x[0].z : x[0].x, word[1] = h ? x[0].w : x[0].y;
           }
-  #pragma unroll
+#pragma unroll
           for (int y = 0; y < WORDS; ++y) {
             T2 c[4];
             Codes<T>::pairs(word[y], c);
@@ -721,13 +724,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 #pragma unroll 1
       for (int j = 0; j < mylen; ++j) {
         const int st = j & 1;
-        const bool both = finite(kv4_pair<BF>(pr));
+        const float2 own = kv4_pair<BF>(pr);
+        const bool both = finite(own);
         if (j >= 2) wait(&sm.v_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
         // transposed: tile row = dim (2b at b, 2b + 1 at D/2 + b), 64 keys per 128-byte atom
         // (s, lo) of this lane's tokens 2t, 2t+1 and 2t+8, 2t+9 in the type
         const uint32_t use = both ? pr : 0u;
         uint32_t q[4];
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < 4; ++e) q[e] = __shfl_sync(0xffffffffu, use, 16 + 2 * t + (e & 1) + 8 * (e >> 1));
         const T2 s0 = kv4_bits<T2>(__byte_perm(q[0], q[1], 0x5410)), l0 = kv4_bits<T2>(__byte_perm(q[0], q[1], 0x7632));
         const T2 s1 = kv4_bits<T2>(__byte_perm(q[2], q[3], 0x5410)), l1 = kv4_bits<T2>(__byte_perm(q[2], q[3], 0x7632));
@@ -735,21 +739,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         const int c0 = (rw & 3) * 2;  // chunk of tokens 0..7 of the record
         uint8_t *v0 = sm.v[st] + (rw / 4) * (D * 128) + g * 128 + 4 * t + ((c0 ^ g) << 4);
         uint8_t *v1 = sm.v[st] + (rw / 4) * (D * 128) + g * 128 + 4 * t + (((c0 + 1) ^ g) << 4);
-  #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-  #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            T2 o[4];  // (dim 2b, tokens 2t..), (2b + 1, 2t..), (2b, 2t+8..), (2b + 1, 2t+8..)
-            Codes<T>::pairs(y[e], o);
-            const int at = (c * 32 + e * 8) * 128;
-            // 15 s + lo can pass the type's largest value (s is rounded): hold it there
-            *reinterpret_cast<T2 *>(v0 + at) = __hmin2(__hfma2(o[0], s0, l0), top);
-            *reinterpret_cast<T2 *>(v0 + at + D * 64) = __hmin2(__hfma2(o[1], s0, l0), top);
-            *reinterpret_cast<T2 *>(v1 + at) = __hmin2(__hfma2(o[2], s1, l1), top);
-            *reinterpret_cast<T2 *>(v1 + at + D * 64) = __hmin2(__hfma2(o[3], s1, l1), top);
+        auto rows = [&](auto clamp) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              T2 o[4];  // (dim 2b, tokens 2t..), (2b + 1, 2t..), (2b, 2t+8..), (2b + 1, 2t+8..)
+              Codes<T>::pairs(y[e], o);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                o[z] = __hfma2(o[z], z < 2 ? s0 : s1, z < 2 ? l0 : l1);
+                if (clamp.value) o[z] = __hmin2(o[z], top);
+                *reinterpret_cast<T2 *>((z < 2 ? v0 : v1) + (c * 32 + e * 8) * 128 + (z & 1) * D * 64) = o[z];
+              }
+            }
           }
-        }
+        };
+        // 15 s + lo can pass the type's largest value (s is rounded): hold it there
+        if (__builtin_expect(__any_sync(0xffffffffu, fmaf(15.f, own.x, own.y) > X::max_finite), 0))
+          rows(std::true_type{});
+        else
+          rows(std::false_type{});
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.v_full[st]);
@@ -764,25 +775,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       constexpr uint32_t id_qk = idesc_f16_f32(128, kKeys) | kind, id_pv = idesc_f16_f32(128, D) | kind;
       auto qk = [&](int i, int jt) {
         const uint64_t qd = sw128_kmajor_desc(smem_u32(sm.q[i])), kd = sw128_kmajor_desc(smem_u32(sm.k[jt & 1]));
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < D / 16; ++x) {
           const uint64_t adv = (x / 4) * (16384 >> 4) + (x % 4) * 2;
-          mma_f16(tm_s[i], qd + adv, kd + adv, id_qk, x > 0);
+          mma_f16(tm_s(i), qd + adv, kd + adv, id_qk, x > 0);
         }
         mma_commit(&sm.s_full[i]);
       };
       auto pv = [&](int i, int jt, bool add) {
         const uint64_t vd = sw128_kmajor_desc(smem_u32(sm.v[jt & 1]));
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < kKeys / 16; ++x) {
           const uint64_t adv = (x / 4) * ((D * 128) >> 4) + (x % 4) * 2;
-          mma_f16_ts(tm_o[i], tm_s[i] + x * 8, vd + adv, id_pv, add || x > 0);
+          mma_f16_ts(tm_o(i), tm_s(i) + x * 8, vd + adv, id_pv, add || x > 0);
         }
         mma_commit(&sm.o_full[i]);
       };
       // Per key tile and row tile: O += P V, then S of the next key tile, which may be the next item's.
       int it = 0, j = 0, n = 0, row_tiles = 0;  // of the tile whose P V comes next
-      uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+      uint32_t p_phase = 0, q_phase = 0;  // a bit per row tile
 #pragma unroll 1
       for (int jt = -1;; ++jt) {
         int next_n = n, next_tiles = row_tiles;
@@ -795,19 +806,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           mbar_arrive(&sm.item_empty[slot]);
         }
         if (row_tiles) wait(&sm.v_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           if (i < row_tiles) {
-            wait(&sm.p_full[i], p_phase[i], &sm.dead, a.status);
-            p_phase[i] ^= 1;
+            wait(&sm.p_full[i], p_phase >> i & 1, &sm.dead, a.status);
+            p_phase ^= 1u << i;
             tc_fence_after();
             pv(i, jt, j > 0);
           }
           if (i < next_tiles) {
             if (i == 0) wait(&sm.k_full[(jt + 1) & 1], ((jt + 1) / 2) & 1, &sm.dead, a.status);
             if (turn) {
-              wait(&sm.q_full[i], q_phase[i], &sm.dead, a.status);
-              q_phase[i] ^= 1;
+              wait(&sm.q_full[i], q_phase >> i & 1, &sm.dead, a.status);
+              q_phase ^= 1u << i;
             }
             tc_fence_after();
             qk(i, jt + 1);
