@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);  // the same in every lane
   auto tm_s = [tmem](int i) { return tmem + i * 128; };
   auto tm_o = [tmem](int i) { return tmem + 256 + i * D; };
 
@@ -769,27 +769,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     }
   } else {
     reg_dec<kRegsMma>();
-    if (warp == 24 && lane == 0) {
+    if (warp == 24) {
       // --------------------------------------------------------------- MMA
       constexpr uint32_t kind = BF ? (1u << 7) | (1u << 10) : 0u;
       constexpr uint32_t id_qk = idesc_f16_f32(128, kKeys) | kind, id_pv = idesc_f16_f32(128, D) | kind;
+      const uint64_t q_desc = sw128_kmajor_desc(smem_u32(sm.q)), k_desc = sw128_kmajor_desc(smem_u32(sm.k)),
+                     v_desc = sw128_kmajor_desc(smem_u32(sm.v));
+      constexpr uint32_t kStage = 128 * D * 2 >> 4;  // an operand tile, in the descriptors' units
       auto qk = [&](int i, int jt) {
-        const uint64_t qd = sw128_kmajor_desc(smem_u32(sm.q[i])), kd = sw128_kmajor_desc(smem_u32(sm.k[jt & 1]));
-#pragma unroll 1
-        for (int x = 0; x < D / 16; ++x) {
-          const uint64_t adv = (x / 4) * (16384 >> 4) + (x % 4) * 2;
-          mma_f16(tm_s(i), qd + adv, kd + adv, id_qk, x > 0);
+        const uint64_t qd = q_desc + i * kStage, kd = k_desc + (jt & 1) * kStage;
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const uint64_t adv = (x / 4) * (16384 >> 4) + (x % 4) * 2;
+            mma_f16(tm_s(i), qd + adv, kd + adv, id_qk, x > 0);
+          }
+          mma_commit(&sm.s_full[i]);
         }
-        mma_commit(&sm.s_full[i]);
+        __syncwarp();
       };
       auto pv = [&](int i, int jt, bool add) {
-        const uint64_t vd = sw128_kmajor_desc(smem_u32(sm.v[jt & 1]));
-#pragma unroll 1
-        for (int x = 0; x < kKeys / 16; ++x) {
-          const uint64_t adv = (x / 4) * ((D * 128) >> 4) + (x % 4) * 2;
-          mma_f16_ts(tm_o(i), tm_s(i) + x * 8, vd + adv, id_pv, add || x > 0);
+        const uint64_t vd = v_desc + (jt & 1) * kStage;
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < kKeys / 16; ++x) {
+            const uint64_t adv = (x / 4) * ((D * 128) >> 4) + (x % 4) * 2;
+            mma_f16_ts(tm_o(i), tm_s(i) + x * 8, vd + adv, id_pv, add || x > 0);
+          }
+          mma_commit(&sm.o_full[i]);
         }
-        mma_commit(&sm.o_full[i]);
+        __syncwarp();
       };
       // Per key tile and row tile: O += P V, then S of the next key tile, which may be the next item's.
       int it = 0, j = 0, n = 0, row_tiles = 0;  // of the tile whose P V comes next
@@ -803,10 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           wait(&sm.item_full[slot], (n ? it + 1 : it) / kItems & 1, &sm.dead, a.status);
           next_n = sm.item[slot].n;
           next_tiles = next_n == 0 || sm.dead ? 0 : sm.item[slot].rows > 128 ? 2 : 1;
-          mbar_arrive(&sm.item_empty[slot]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
         }
         if (row_tiles) wait(&sm.v_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (i < row_tiles) {
             wait(&sm.p_full[i], p_phase >> i & 1, &sm.dead, a.status);
@@ -824,9 +834,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             qk(i, jt + 1);
           }
         }
-        if (row_tiles) mma_commit(&sm.v_empty[jt & 1]);
+        if (row_tiles && elect_one()) mma_commit(&sm.v_empty[jt & 1]);
+        __syncwarp();
         if (!next_tiles) break;
-        mma_commit(&sm.k_empty[(jt + 1) & 1]);
+        if (elect_one()) mma_commit(&sm.k_empty[(jt + 1) & 1]);
+        __syncwarp();
         if (turn) {
           if (n) ++it;
           j = 0;
@@ -836,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         n = next_n;
         row_tiles = next_tiles;
       }
-      mma_commit(&sm.done);  // nothing in flight when the CTA gives its memory back
+      if (elect_one()) mma_commit(&sm.done);  // nothing in flight when the CTA gives its memory back
       mbar_wait(&sm.done, 0, kWaitNs);
     } else if (warp == 25) {
       // -------------------------------------------------------------- walk

@@ -236,6 +236,19 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
       : "memory");
 }
 
+// One lane of a converged warp.  Code under it keeps warp-uniform operands in
+// uniform registers, which one lane of a diverged warp would have to move there
+// for every instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(one));
+  return one != 0;
+}
+
 // D(tmem, int32) (+)= A(tmem, s8, K-major: lane = row, 4 K values per 32-bit
 // column) * B(smem, s8, K-major)^T
 __device__ __forceinline__ void mma_i8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
