@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       if (n == 0 || sm.dead) break;
       const bool active = i * 128 < x.rows;
       uint64_t la = pack2(0.f, 0.f), lb = la;
-      float base = 0.f;         // what is added to t: 6 - m once a key was seen
+      float base = 0.f;         // what is added to t: 6 - m, m a whole number, once a key was seen
       float limit = -INFINITY;  // t + base above this moves the maximum
       if (active) {
         const bool valid = r < x.rows;
@@ -507,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           // first c chunks of weights
           auto grow = [&](Chunk &t, int c, float mx) {
             const bool need = mx > limit;
-            const float d = need ? 6.f - mx : 0.f;
-            const float al = limit > -INFINITY ? ex2f(d) : 1.f;  // nothing to scale before the first key
+            const float d = need ? 6.f - ceilf(mx) : 0.f;
+            const float al = limit > -INFINITY ? ex2f(d) : 1.f;  // a power of two; nothing to scale before the first key
             if (need) limit = 14.f;
             base += d;
             const uint64_t d2 = pack2(d, d), al2 = pack2(al, al);
