@@ -14,13 +14,17 @@
 // instruction.  Everything a warp touches of a record is contiguous per lane
 // (layout in kv4.h): two 16-byte shared loads for K, two for V.
 //
-// The cache is read once: HBM bounds the kernel.  Each warp keeps its own ring
-// of records in flight (one bulk copy each, one mbarrier per slot), so no warp
-// waits for another in the loop.  The records of all (sequence, head, row
-// tile) items are one line, cut into equal parts over a persistent grid: the
-// load is even whatever the lengths, and the host needs to know none of them.
-// An item cut by such a boundary leaves fp32 partial results in the workspace,
-// which a second, dependent launch joins in the order of the parts.
+// The cache is read once: HBM bounds the kernel, if the instructions per record
+// stay few.  So a warp takes units of two records, looks pages up for 16 units at
+// a time (a record a lane), and checks the running maximum by the sum of the
+// weights.  Each warp keeps its own ring of units in flight (a bulk copy a record,
+// one mbarrier per slot).  The units of all (sequence, head, row tile) items are
+// one line, cut into equal parts over a persistent grid and each CTA's part again
+// over its warps: the load is even whatever the lengths, the host needs to know
+// none of them, and no warp waits for another before its span is done.
+// An item cut between warps is joined in shared memory at the CTA's end; one cut
+// between CTAs leaves fp32 partial results in the workspace, which a second,
+// dependent launch joins in the order of the parts.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -36,7 +40,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr float kNegBig = -1e30f;  // running maximum before the first visible key
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMinQuota = 16;  // records: below two a warp, a cut costs more than it spreads
+constexpr int kUnit = 2;       // records
+constexpr int kUnitKeys = kUnit * kKv4Rec;
+constexpr int kMinQuota = 8;   // units: below one a warp, a cut costs more than it spreads
 constexpr int kMaxRows = 16;
 
 struct Desc {  // item whose last part is not in the CTA that starts it
@@ -51,8 +57,8 @@ struct Seq {
   int len;          // keys that exist (bounded by the table)
   int pos0;         // position of the first new token
   int tiles;        // row tiles per kv head
-  int n_rec;        // records visited per item (at least 1 if there are rows)
-  int skip_at, skip_by;  // record index i >= skip_at means record i + skip_by
+  int n_unit;       // units visited per item (at least 1 if there are rows)
+  int skip_at, skip_by;  // unit index i >= skip_at means unit i + skip_by
 };
 
 template <int R>
@@ -71,23 +77,23 @@ __device__ __forceinline__ Seq load_seq(const Kv4AttnArgs &a, int s) {
   q.pos0 = full - q.nq;
   const int64_t rows = static_cast<int64_t>(q.nq) * a.group;
   q.tiles = rows > a.tile_above ? 0 : static_cast<int>((rows + R - 1) / R);
-  const int total = (q.len + kKv4Rec - 1) / kKv4Rec;
+  const int total = static_cast<int>((static_cast<unsigned>(q.len) + kUnitKeys - 1) / kUnitKeys);
   q.skip_at = total;
   q.skip_by = 0;
-  q.n_rec = total;
+  q.n_unit = total;
   if (a.window > 0) {
-    const int first = max(0, max(q.pos0, 0) - a.window + 1) / kKv4Rec;  // first record of the window
-    const int sink = min((min(a.sinks, q.len) + kKv4Rec - 1) / kKv4Rec, first);
+    const int first = max(0, max(q.pos0, 0) - a.window + 1) / kUnitKeys;  // first unit of the window
+    const int sink = min(static_cast<int>((static_cast<unsigned>(min(a.sinks, q.len)) + kUnitKeys - 1) / kUnitKeys), first);
     q.skip_at = sink;
     q.skip_by = min(first, total) - sink;
-    q.n_rec = total - q.skip_by;
+    q.n_unit = total - q.skip_by;
   }
-  q.n_rec = max(q.n_rec, 1);
+  q.n_unit = max(q.n_unit, 1);
   return q;
 }
 
 __device__ __forceinline__ int64_t seq_cost(const Seq &q, int n_kv) {
-  return static_cast<int64_t>(q.tiles) * n_kv * q.n_rec;
+  return static_cast<int64_t>(q.tiles) * n_kv * q.n_unit;
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -117,7 +123,7 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
-// Position on the line of records, relative to the CTA's first record.
+// Position on the line of units, relative to the CTA's first unit.
 template <int R>
 struct Walk {
   Seq q;
@@ -126,9 +132,11 @@ struct Walk {
   __device__ __forceinline__ int items(const Kv4AttnArgs &a) const { return q.tiles * a.c.n_kv; }
   // to the item that holds position i (the caller keeps i below the CTA's end)
   __device__ __forceinline__ void seek(const Kv4AttnArgs &a, int i) {
-    while (i >= start + q.n_rec) {
-      start += q.n_rec;
-      if (++item >= items(a)) {
+    while (i >= start + q.n_unit) {
+      const int by = min((i - start) / q.n_unit, items(a) - item);
+      start += by * q.n_unit;
+      item += by;
+      if (item == items(a)) {
         item = 0;
         do {
           q = load_seq<R>(a, ++seq);
@@ -137,10 +145,15 @@ struct Walk {
     }
   }
   __device__ __forceinline__ int head(const Kv4AttnArgs &) const { return item / q.tiles; }
-  __device__ __forceinline__ int record(int i) const {
+  __device__ __forceinline__ int unit(int i) const {
     const int r = i - start;
     return r + (r >= q.skip_at ? q.skip_by : 0);
   }
+};
+
+struct Place {  // of a part of an item
+  int seq, item, end;  // where the item ends in the CTA's part of the line
+  int head, row0, row_first, rows;  // first q row of the sequence, first row and number of rows of the item
 };
 
 template <int D, int NT, int SLOTS>
@@ -148,14 +161,16 @@ struct Smem {
   static constexpr int REC = kv4_rec_bytes(D);
   static constexpr int R = 8 * NT;
   static constexpr int OROW = D + 4;  // padded row: float2 stores of the four t lanes hit other banks
-  alignas(128) uint8_t ring[kWarps][SLOTS][REC];
-  alignas(16) float o[kWarps][R][OROW];
-  float m[kWarps][R], l[kWarps][R];
+  alignas(128) uint8_t ring[kWarps][SLOTS][kUnit][REC];
+  float m[2][kWarps][R], l[2][kWarps][R];  // [0]: the item that a warp's span begins in, [1]: the one it ends in
+  int part[kWarps];                        // bit 0: the first is there, 1: and ends here, 2: the second is there, 3: no span
+  Place place[2][kWarps];
   uint64_t full[kWarps][SLOTS];
-  int ok[kWarps][SLOTS];
+  int ok[kWarps][SLOTS];  // a bit per record
   long long scan[kWarps + 1];
   int found_seq;
   long long found_start;
+  long long lo, quota;
 };
 
 template <typename T, int D, int NT, int SLOTS>
@@ -173,30 +188,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
   griddep_launch_dependents();
 
   // ---- this CTA's part of the line
-  long long mine = 0;
-  for (int s = tid; s < a.b.n_seqs; s += kThreads) mine += seq_cost(load_seq<R>(a, s), a.c.n_kv);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sm.scan[warp] = mine;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long quota = per > kMinQuota ? per : kMinQuota;
-  const long long lo = min(static_cast<long long>(blockIdx.x) * quota, total);
-  const int mylen = static_cast<int>(min(quota, total - lo));
-  Desc *desc = reinterpret_cast<Desc *>(a.work);
-  float *slots = a.work + gridDim.x * (sizeof(Desc) / 4);
-  if (mylen == 0) {
-    if (tid == 0) desc[blockIdx.x].seq = -1;
-    return;
-  }
-  // the sequence that holds position lo
-  long long base = 0;
-  for (int s0 = 0; s0 < a.b.n_seqs; s0 += kThreads) {
+  long long total = 0, cost = 0, start = 0;  // of the thread's last sequence
+  auto scan = [&](int s0) {
     const int s = s0 + tid;
-    const long long cost = s < a.b.n_seqs ? seq_cost(load_seq<R>(a, s), a.c.n_kv) : 0;
+    cost = s < a.b.n_seqs ? seq_cost(load_seq<R>(a, s), a.c.n_kv) : 0;
     long long incl = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -206,19 +201,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     __syncthreads();
     if (lane == 31) sm.scan[warp] = incl;
     __syncthreads();
-    long long before = base, all = 0;
+    start = total + incl - cost;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sm.scan[w];
-      all += sm.scan[w];
+      if (w < warp) start += sm.scan[w];
+      total += sm.scan[w];
     }
-    const long long start = before + incl - cost;
+  };
+  for (int s0 = 0; s0 < a.b.n_seqs; s0 += kThreads) scan(s0);
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long quota = per > kMinQuota ? per : kMinQuota;
+  const long long lo = min(static_cast<long long>(blockIdx.x) * quota, total);
+  const int mylen = static_cast<int>(min(quota, total - lo));
+  Desc *desc = reinterpret_cast<Desc *>(a.work);
+  auto slots = [&]() { return a.work + gridDim.x * (sizeof(Desc) / 4); };
+  auto heads = [&]() { return slots() + 2 * gridDim.x * slot_floats(D) + static_cast<size_t>(blockIdx.x) * kWarps * R * D; };
+  if (tid == 0) sm.lo = lo, sm.quota = quota;  // kept there, not in registers
+  if (mylen == 0) {
+    if (tid == 0) desc[blockIdx.x].seq = -1;
+    return;
+  }
+  // the sequence that holds position lo
+  auto find = [&](int s0) {
     if (lo >= start && lo < start + cost) {
-      sm.found_seq = s;
+      sm.found_seq = s0 + tid;
       sm.found_start = start;
     }
-    base += all;
-    if (base > lo) break;
+  };
+  if (a.b.n_seqs <= kThreads) {
+    find(0);
+  } else {
+    total = 0;
+    for (int s0 = 0; total <= lo; s0 += kThreads) {
+      scan(s0);
+      find(s0);
+    }
   }
   __syncthreads();
 
@@ -227,67 +244,82 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
   cur.q = load_seq<R>(a, cur.seq);
   {
     const long long in = lo - sm.found_start;
-    cur.item = static_cast<int>(in / cur.q.n_rec);
-    cur.start = static_cast<int>(static_cast<long long>(cur.item) * cur.q.n_rec - in);
+    cur.item = static_cast<int>(in / cur.q.n_unit);
+    cur.start = static_cast<int>(static_cast<long long>(cur.item) * cur.q.n_unit - in);
   }
 
-  // ---- the warp's ring.  Two steps ahead of the copy: the page of the next
-  // record is loaded one turn before its copy is issued.
-  Walk<R> pre = cur;
-  int pre_i = warp;       // position whose page is in pre_page
+  // ---- the warp's span [w0, w1) of the part, and its ring.  Lane 2 u + r has the place of record r of
+  // the u-th unit of a batch of 16, and the page of the same one of the next batch.
+  // Warp 0 always has one.
+  const int w0 = static_cast<int>((static_cast<int64_t>(mylen) * warp + kWarps - 1) / kWarps),
+            w1 = static_cast<int>((static_cast<int64_t>(mylen) * (warp + 1) + kWarps - 1) / kWarps);
+  int pre_i = w0 + lane / kUnit;
   int pre_page = -1;
-  int64_t pre_off = 0;
-  uint32_t issued = 0;
+  int64_t pre_off = -1, place = -1;  // -1: beyond the keys, -2: the page is not usable
   const uint64_t policy = policy_evict_first();
-  auto load_page = [&]() {
-    pre_page = -1;
-    if (pre_i >= mylen) return;
-    pre.seek(a, pre_i);
-    const int rec = pre.record(pre_i);
-    if (rec * kKv4Rec >= pre.q.len) return;
-    const int slot = a.c.page_shift >= 0 ? rec >> a.c.page_shift : rec / a.c.recs_per_page;
-    pre_page = __ldg(a.b.table + pre.seq * a.b.table_stride + slot);
-    pre_off = (static_cast<int64_t>(pre.head(a)) * a.c.recs_per_page + (rec - slot * a.c.recs_per_page)) * REC;
-  };
-  auto issue = [&]() {
-    if (pre_i < mylen) {
-      if (lane == 0) {
-        const int slot = issued % SLOTS;
-        uint64_t *bar = &sm.full[warp][slot];
-        const bool ok = pre_page >= 0 && pre_page < a.c.n_pages;
-        sm.ok[warp][slot] = ok;
-        if (ok) {
-          mbar_arrive_expect_tx(bar, REC);
-          bulk_load(sm.ring[warp][slot], a.c.pages + pre_page * a.c.page_stride + pre_off, REC, bar, policy);
-        } else {
-          if (pre.q.len > 0 && pre.record(pre_i) * kKv4Rec < pre.q.len) record_error(a.status, kErrInvalidArg);
-          mbar_arrive(bar);
-        }
+  auto look_up = [&]() {
+    pre_off = -1;
+    if (pre_i < w1) {
+      Walk<R> pre = cur;  // at most a batch and a ring behind
+      pre.seek(a, pre_i);
+      const int64_t rec = static_cast<int64_t>(pre.unit(pre_i)) * kUnit + lane % kUnit;
+      if (rec * kKv4Rec < pre.q.len) {
+        const int r = static_cast<int>(rec), slot = a.c.page_shift >= 0 ? r >> a.c.page_shift : r / a.c.recs_per_page;
+        pre_page = __ldg(a.b.table + pre.seq * a.b.table_stride + slot);
+        pre_off = (static_cast<int64_t>(pre.head(a)) * a.c.recs_per_page + (r - slot * a.c.recs_per_page)) * REC;
       }
-      ++issued;
-      pre_i += kWarps;
     }
-    load_page();
+    pre_i += 32 / kUnit;
   };
-  load_page();
+  auto issue = [&](int n) {  // the span's n-th unit
+    const int u = n % (32 / kUnit), slot = n % SLOTS;
+    if (u == 0) {
+      place = pre_off;
+      if (pre_off >= 0) {
+        place = pre_page >= 0 && pre_page < a.c.n_pages ? pre_page * a.c.page_stride + pre_off : -2;
+        if (place < 0) record_error(a.status, kErrInvalidArg);
+      }
+      look_up();
+    }
+    const int64_t p0 = __shfl_sync(0xffffffffu, place, kUnit * u), p1 = __shfl_sync(0xffffffffu, place, kUnit * u + 1);
+    if (elect_one()) {
+      uint64_t *bar = &sm.full[warp][slot];
+      uint8_t(*dst)[REC] = sm.ring[warp][slot];
+      sm.ok[warp][slot] = (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0);
+      if (p0 >= 0 && p1 == p0 + REC) {  // neighbours in a page
+        mbar_arrive_expect_tx(bar, 2 * REC);
+        bulk_load(dst[0], a.c.pages + p0, 2 * REC, bar, policy);
+      } else {
+        const uint32_t bytes = (p0 >= 0 ? REC : 0) + (p1 >= 0 ? REC : 0);
+        if (bytes)
+          mbar_arrive_expect_tx(bar, bytes);
+        else
+          mbar_arrive(bar);
+        if (p0 >= 0) bulk_load(dst[0], a.c.pages + p0, REC, bar, policy);
+        if (p1 >= 0) bulk_load(dst[1], a.c.pages + p1, REC, bar, policy);
+      }
+    }
+    __syncwarp();
+  };
+  look_up();
 #pragma unroll 1
-  for (int i = 0; i < SLOTS; ++i) issue();
+  for (int i = 0; i < SLOTS; ++i)
+    if (w0 + i < w1) issue(i);
 
-  uint32_t used = 0;
   bool dead = false;
   const float sl2 = a.scale * 1.4426950408889634f;
 
+  int parts = w0 < w1 ? 0 : 8;
 #pragma unroll 1
-  for (int pos = 0; pos < mylen;) {
+  for (int pos = w0; pos < w1;) {
     cur.seek(a, pos);
-    const int seg_end = min(cur.start + cur.q.n_rec, mylen);
+    const int seg_end = min(cur.start + cur.q.n_unit, w1);
     const int head = cur.head(a), tile = cur.item - head * cur.q.tiles;
     const int row_first = tile * R, rows_all = cur.q.nq * a.group;
 
     // ---- query fragments: column n = query row, lane t holds dims [t D/4, (t+1) D/4)
     uint32_t qf[NT][WORDS][4];
     float cs[NT][2], qs[NT][2];
-    int vis[NT][2], wlo[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row_first + nt * 8 + g;
@@ -343,16 +375,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const float up = sl2 * (BF ? pow2(e) : 1.f);
       const float mycs = up * 16777216.f, myqs = up * sum;
-      const int p = cur.q.pos0 + qi;
-      const int myvis = valid ? min(p + 1, cur.q.len) : 0x7fffffff;
-      const int mywlo = valid && a.window > 0 ? max(p, 0) - a.window + 1 : -0x7fffffff;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int src = (2 * t + j) * 4;
         cs[nt][j] = __shfl_sync(0xffffffffu, mycs, src);
         qs[nt][j] = __shfl_sync(0xffffffffu, myqs, src);
-        vis[nt][j] = __shfl_sync(0xffffffffu, myvis, src);
-        wlo[nt][j] = __shfl_sync(0xffffffffu, mywlo, src);
       }
     }
     // positions of the tile's first and last row
@@ -363,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     const int edge_min = max(pmin, 0) - a.window, edge_max = max(pmax, 0) - a.window;
 
     float o[NT][MT][4], m[NT][2], l[NT][2], z[NT][2];
+    float lim[NT][2];  // a sum of weights above this moves the maximum m (0 before the first key)
     float sig = pow2(100);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -372,97 +400,123 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        m[nt][j] = kNegBig;
+        m[nt][j] = 0.f;
+        lim[nt][j] = -1.f;
         l[nt][j] = 0.f;
         z[nt][j] = 0.f;
       }
     }
 
-    // ---- the warp's records of this segment
+    // ---- the warp's units of this segment
 #pragma unroll 1
-    for (int i = pos + ((warp - pos) & (kWarps - 1)); i < seg_end; i += kWarps) {
-      const int slot = used % SLOTS;
-      if (!dead && !mbar_wait(&sm.full[warp][slot], (used / SLOTS) & 1, kWaitNs)) {
+    for (int i = pos; i < seg_end; ++i) {
+      const int slot = (i - w0) % SLOTS;
+      if (!dead && !mbar_wait(&sm.full[warp][slot], (i - w0) / SLOTS & 1, kWaitNs)) {
         dead = true;
         if (lane == 0) record_error(a.status, kErrTimeout);
       }
-      ++used;
-      const uint8_t *rec = sm.ring[warp][slot];
-      const bool ok = sm.ok[warp][slot] && !dead;
-      const int j0 = cur.record(i) * kKv4Rec;
-      const bool none = !ok || j0 > pmax || (a.window > 0 && j0 + kKv4Rec <= edge_min + 1 && j0 >= a.sinks);
+      const int ok = dead ? 0 : sm.ok[warp][slot];
+      const int j0 = cur.unit(i) * kUnitKeys;
+      const bool none = !ok || j0 > pmax || (a.window > 0 && j0 + kUnitKeys <= edge_min + 1 && j0 >= a.sinks);
       if (!none) {
-        uint32_t ka[WORDS], kb[WORDS], vw[WORDS * 2];
-        if (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(rec + lane * 16);
-          const uint4 y = *reinterpret_cast<const uint4 *>(rec + 512 + lane * 16);
-          ka[0] = x.x, ka[1] = x.y, ka[WORDS - 2] = x.z, ka[WORDS - 1] = x.w;
-          kb[0] = y.x, kb[1] = y.y, kb[WORDS - 2] = y.z, kb[WORDS - 1] = y.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2 *>(rec + lane * 8);
-          const uint2 y = *reinterpret_cast<const uint2 *>(rec + 256 + lane * 8);
-          ka[0] = x.x, ka[1] = x.y, kb[0] = y.x, kb[1] = y.y;
-        }
+        // scores, less the maxima, of tokens g and g + 8 of each record for columns 2t, 2t + 1
+        float s[kUnit][NT][4], vs[kUnit][2], vl[kUnit][2];
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(rec + 8 * D + c * 512 + lane * 16);
-          vw[4 * c] = x.x, vw[4 * c + 1] = x.y, vw[4 * c + 2] = x.z, vw[4 * c + 3] = x.w;
-        }
-        const uint32_t *pk = reinterpret_cast<const uint32_t *>(rec + 16 * D);
-        float2 kp0 = kv4_pair<BF>(pk[g]), kp1 = kv4_pair<BF>(pk[g + 8]);
-        // an infinite pair makes the score NaN, not one more hidden key at -inf
-        kp0.x = fmaf(kp0.x + kp0.y, 0.f, kp0.x);
-        kp1.x = fmaf(kp1.x + kp1.y, 0.f, kp1.x);
-        const float2 v0 = kv4_pair<BF>(pk[16 + g]), v1 = kv4_pair<BF>(pk[24 + g]);
-
-        // scores of tokens g and g + 8 for columns 2t, 2t + 1
-        float s[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < WORDS; ++w) {
-            const uint32_t a8 = ka[w] >> 8, b8 = kb[w] >> 8;
-            mma16816(x, ka[w] & 0x000f000fu, kb[w] & 0x000f000fu, a8 & 0x000f000fu,
-                     b8 & 0x000f000fu, qf[nt][w][0], qf[nt][w][2]);
-            mma16816(y, ka[w] & 0x00f000f0u, kb[w] & 0x00f000f0u, a8 & 0x00f000f0u,
-                     b8 & 0x00f000f0u, qf[nt][w][1], qf[nt][w][3]);
+        for (int r = 0; r < kUnit; ++r) {
+          const uint8_t *rec = sm.ring[warp][slot][r];
+          uint32_t ka[WORDS], kb[WORDS];
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(rec + lane * 16);
+            const uint4 y = *reinterpret_cast<const uint4 *>(rec + 512 + lane * 16);
+            ka[0] = x.x, ka[1] = x.y, ka[WORDS - 2] = x.z, ka[WORDS - 1] = x.w;
+            kb[0] = y.x, kb[1] = y.y, kb[WORDS - 2] = y.z, kb[WORDS - 1] = y.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(rec + lane * 8);
+            const uint2 y = *reinterpret_cast<const uint2 *>(rec + 256 + lane * 8);
+            ka[0] = x.x, ka[1] = x.y, kb[0] = y.x, kb[1] = y.y;
           }
+          const uint32_t *pk = reinterpret_cast<const uint32_t *>(rec + 16 * D);
+          float2 kp0 = kv4_pair<BF>(pk[g]), kp1 = kv4_pair<BF>(pk[g + 8]);
+          // an infinite pair makes the score NaN, not one more hidden key at -inf
+          kp0.x = fmaf(kp0.x + kp0.y, 0.f, kp0.x);
+          kp1.x = fmaf(kp1.x + kp1.y, 0.f, kp1.x);
+          const float2 v0 = kv4_pair<BF>(pk[16 + g]), v1 = kv4_pair<BF>(pk[24 + g]);
+          vs[r][0] = v0.x, vs[r][1] = v1.x, vl[r][0] = v0.y, vl[r][1] = v1.y;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 k = j < 2 ? kp0 : kp1;
-            const float raw = fmaf(y[j], 0.0625f, x[j]);
-            s[nt][j] = fmaf(raw * k.x, cs[nt][j & 1], k.y * qs[nt][j & 1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) {
+              const uint32_t a8 = ka[w] >> 8, b8 = kb[w] >> 8;
+              mma16816(x, ka[w] & 0x000f000fu, kb[w] & 0x000f000fu, a8 & 0x000f000fu,
+                       b8 & 0x000f000fu, qf[nt][w][0], qf[nt][w][2]);
+              mma16816(y, ka[w] & 0x00f000f0u, kb[w] & 0x00f000f0u, a8 & 0x00f000f0u,
+                       b8 & 0x00f000f0u, qf[nt][w][1], qf[nt][w][3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 k = j < 2 ? kp0 : kp1;
+              const float raw = fmaf(y[j], 0.0625f, x[j]);
+              s[r][nt][j] = fmaf(raw * k.x, cs[nt][j & 1], fmaf(k.y, qs[nt][j & 1], -m[nt][j & 1]));
+            }
           }
         }
-        const bool whole = j0 + kKv4Rec <= min(pmin + 1, cur.q.len) &&
-                           (a.window <= 0 || j0 > edge_max || j0 + kKv4Rec <= a.sinks);
-        float s0 = v0.x, s1 = v1.x, l0 = v0.y, l1 = v1.y;
+        const bool whole = ok == 3 && j0 <= min(pmin + 1, cur.q.len) - kUnitKeys &&
+                           (a.window <= 0 || j0 > edge_max || j0 + kUnitKeys <= a.sinks);
         if (!whole) {
+          const int last = min(pmax, cur.q.len - 1);
+          // a column's row sees key j when j < vis and (j >= wlo or j < sinks); columns without a row
+          // see all
+          int vis[NT][2], wlo[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int key = j0 + g + (j < 2 ? 0 : 8);
-              if (key >= vis[nt][j & 1] || (key < wlo[nt][j & 1] && key >= a.sinks)) s[nt][j] = -INFINITY;
+            for (int j = 0; j < 2; ++j) {
+              const int rr = row_first + nt * 8 + 2 * t + j, p = cur.q.pos0 + rr / a.group;
+              const bool valid = rr < rows_all;
+              vis[nt][j] = valid ? min(p + 1, cur.q.len) : 0x7fffffff;
+              wlo[nt][j] = valid && a.window > 0 ? max(p, 0) - a.window + 1 : 0;
             }
-          // tokens that no row of the tile sees may hold anything
-          const int k0 = j0 + g, k1 = k0 + 8, last = min(pmax, cur.q.len - 1);
-          if (k0 > last || (a.window > 0 && k0 <= edge_min && k0 >= a.sinks)) s0 = 0.f, l0 = 0.f;
-          if (k1 > last || (a.window > 0 && k1 <= edge_min && k1 >= a.sinks)) s1 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int r = 0; r < kUnit; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = j0 + r * kKv4Rec + h * 8 + g;
+              const bool gone = !(ok >> r & 1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (gone || key >= vis[nt][j] || (key < wlo[nt][j] && key >= a.sinks)) s[r][nt][2 * h + j] = -INFINITY;
+              // tokens that no row of the tile sees may hold anything
+              if (gone || key > last || (a.window > 0 && key <= edge_min && key >= a.sinks)) vs[r][h] = 0.f, vl[r][h] = 0.f;
+            }
         }
 
-        // ---- running maximum, moved only when a score passes it by 2^8
-        bool grow = false;
+        // ---- weights.  No weight is above its column's sum, so the sums tell whether a maximum has
+        // to move: when a score passes it by about 2^8.  V scales go to [2^6, 2^7) of the largest
+        // seen, so weights times scale stay below 2^15 and keep fp16's 11 bits down to 2^-21 of
+        // the largest.
+        float p[kUnit][NT][4], sum[NT][2];
+        auto weigh = [&]() -> bool {
+          bool over = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) grow |= s[nt][j] > m[nt][j & 1] + 8.f;
-        // V scales go to [2^6, 2^7) of the largest seen, so weights times scale
-        // stay below 2^15 and keep fp16's 11 bits down to 2^-21 of the largest
-        const float smax = fmaxf(s0, s1);
-        const bool rescale = smax * sig >= 128.f;
-        if (__any_sync(0xffffffffu, grow || rescale)) {
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+              for (int r = 0; r < kUnit; ++r) {
+                p[r][nt][j] = ex2(s[r][nt][j]);
+                p[r][nt][j + 2] = ex2(s[r][nt][j + 2]);
+              }
+              sum[nt][j] = (p[0][nt][j] + p[0][nt][j + 2]) + (p[1][nt][j] + p[1][nt][j + 2]);
+              over |= sum[nt][j] > lim[nt][j];
+            }
+          return over;
+        };
+        const float smax = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+        const bool over = weigh();
+        if (__any_sync(0xffffffffu, over || smax * sig >= 128.f)) {
           float f = 1.f;
           float mx = smax < INFINITY ? fmaxf(smax, 0.f) : 0.f;
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -478,13 +532,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             float al[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float n = fmaxf(s[nt][j], s[nt][j + 2]);
+              float n = fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]), fmaxf(s[1][nt][j], s[1][nt][j + 2]));
               n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
               n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
               n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16));
-              n = fmaxf(n, m[nt][j]);
-              al[j] = ex2(m[nt][j] - n);
-              m[nt][j] = n;
+              const bool seen = lim[nt][j] > 0.f;
+              const float d = n > (seen ? 0.f : -INFINITY) ? n : 0.f;
+              al[j] = seen ? ex2(-d) : 1.f;  // nothing to scale before the first key
+              if (n > -INFINITY) lim[nt][j] = 256.f;
+              m[nt][j] += d;
+#pragma unroll
+              for (int r = 0; r < kUnit; ++r) {
+                s[r][nt][j] -= d;
+                s[r][nt][j + 2] -= d;
+              }
               l[nt][j] *= al[j];
               z[nt][j] *= al[j];
               al[j] *= f;
@@ -497,55 +558,72 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
               o[nt][i][3] *= al[1];
             }
           }
+          weigh();
         }
 
-        // ---- weights, their sums, and the products with V
-        s0 *= sig;
-        s1 *= sig;
-        uint32_t p0[NT], p1[NT];
+        // ---- their sums, and the products with V
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
+        for (int r = 0; r < kUnit; ++r) {
+          uint32_t p0[NT], p1[NT];
+          const float s0 = vs[r][0] * sig, s1 = vs[r][1] * sig;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            p[j] = ex2(s[nt][j] - m[nt][j & 1]);
-            l[nt][j & 1] += p[j];
-          }
-          float w[4];
-          if (whole) {
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+            if (whole) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              z[nt][j & 1] = fmaf(p[j], j < 2 ? l0 : l1, z[nt][j & 1]);
-              w[j] = p[j] * (j < 2 ? s0 : s1);
+              for (int j = 0; j < 4; ++j) {
+                z[nt][j & 1] = fmaf(p[r][nt][j], vl[r][j / 2], z[nt][j & 1]);
+                w[j] = p[r][nt][j] * (j < 2 ? s0 : s1);
+              }
+            } else {
+              // a key hidden from this row must not reach it through 0 * NaN
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool hid = s[r][nt][j] == -INFINITY;
+                z[nt][j & 1] += hid ? 0.f : p[r][nt][j] * vl[r][j / 2];
+                w[j] = hid ? 0.f : p[r][nt][j] * (j < 2 ? s0 : s1);
+              }
             }
-          } else {
-            // a key hidden from this row must not reach it through 0 * NaN
+            if (r == 0) {
+              l[nt][0] += sum[nt][0];
+              l[nt][1] += sum[nt][1];
+            }
+            p0[nt] = transpose8x8(pack_half2(w[0], w[1]));
+            p1[nt] = transpose8x8(pack_half2(w[2], w[3]));
+          }
+          const uint8_t *rec = sm.ring[warp][slot][r];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const bool hid = s[nt][j] == -INFINITY;
-              z[nt][j & 1] += hid ? 0.f : p[j] * (j < 2 ? l0 : l1);
-              w[j] = hid ? 0.f : p[j] * (j < 2 ? s0 : s1);
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(rec + 8 * D + c * 512 + lane * 16);
+            const uint32_t vw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t v8 = vw[i] >> 8;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(o[nt][4 * c + i], vw[i] & 0x000f000fu, vw[i] & 0x00f000f0u, v8 & 0x000f000fu,
+                         v8 & 0x00f000f0u, p0[nt], p1[nt]);
             }
           }
-          p0[nt] = transpose8x8(pack_half2(w[0], w[1]));
-          p1[nt] = transpose8x8(pack_half2(w[2], w[3]));
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const uint32_t v8 = vw[i] >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(o[nt][i], vw[i] & 0x000f000fu, vw[i] & 0x00f000f0u, v8 & 0x000f000fu,
-                     v8 & 0x00f000f0u, p0[nt], p1[nt]);
         }
       }
       __syncwarp();
-      issue();
+      if (i + SLOTS < w1) issue(i + SLOTS - w0);
     }
 
-    // ---- join the warps.  Rows 8 m + g of the products are dims 2 (8 m + g) (x 2^-24)
-    // and 2 (8 m + g) + 1 (x 2^-20).
+    // ---- the segment's result.  Rows 8 i + g of the products are dims 2 (8 i + g) (x 2^-24) and
+    // 2 (8 i + g) + 1 (x 2^-20).
     const float un = 1.f / sig;
+    const bool begins = cur.start >= w0, ends = cur.start + cur.q.n_unit <= w1;
+    // the second kind waits in the ring, which is empty by then; the first would be in its way
+    const int which = begins ? 1 : 0;
+    float *part = begins ? reinterpret_cast<float *>(sm.ring[warp]) : heads() + warp * (R * D);
+    const int pitch = begins ? S::OROW : D;
+    if (!begins) parts |= ends ? 3 : 1;
+    if (begins && !ends) parts |= 4;
+    if (lane == 0 && !(begins && ends))
+      sm.place[which][warp] = Place{cur.seq, cur.item, cur.start + cur.q.n_unit, head, cur.q.row0, row_first,
+                                    min(R, rows_all - row_first)};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -556,42 +634,78 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
           lj += __shfl_xor_sync(0xffffffffu, lj, x);
           zj += __shfl_xor_sync(0xffffffffu, zj, x);
         }
-        const int col = nt * 8 + 2 * t + j;
+        const int col = nt * 8 + 2 * t + j, rr = row_first + col;
+        if (rr >= rows_all) continue;
+        if (begins && ends) {
+          const float inv = lj == 0.f ? 0.f : 1.f / lj;
+          const int qi = rr / a.group;
+          T *op = static_cast<T *>(a.out) + (cur.q.row0 + static_cast<int64_t>(qi)) * a.o_row +
+                  (static_cast<int64_t>(head) * a.group + (rr - qi * a.group)) * a.o_head + 2 * g;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          *reinterpret_cast<float2 *>(&sm.o[warp][col][2 * (8 * i + g)]) =
-              make_float2(fmaf(o[nt][i][j] * 16777216.f, un, zj), fmaf(o[nt][i][j + 2] * 1048576.f, un, zj));
-        if (g == 0) {
-          sm.m[warp][col] = m[nt][j];
-          sm.l[warp][col] = lj;
+          for (int i = 0; i < MT; ++i)
+            *reinterpret_cast<uint32_t *>(op + 16 * i) = kv4_bits<uint32_t>(
+                Kv4Type<T>::from2(fmaf(o[nt][i][j] * 16777216.f, un, zj) * inv, fmaf(o[nt][i][j + 2] * 1048576.f, un, zj) * inv));
+        } else {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            *reinterpret_cast<float2 *>(part + col * pitch + 2 * (8 * i + g)) =
+                make_float2(fmaf(o[nt][i][j] * 16777216.f, un, zj), fmaf(o[nt][i][j + 2] * 1048576.f, un, zj));
+          if (g == 0) {
+            sm.m[which][warp][col] = lim[nt][j] > 0.f ? m[nt][j] : kNegBig;
+            sm.l[which][warp][col] = lj;
+          }
         }
       }
-    __syncthreads();
-    const bool begins = cur.start >= 0, ends = cur.start + cur.q.n_rec <= mylen;
-    float *part = slots + (2 * blockIdx.x + (begins ? 1 : 0)) * slot_floats(D);
-    for (int e = tid; e < R * D / 4; e += kThreads) {
+    pos = seg_end;
+  }
+  if (lane == 0) sm.part[warp] = parts;
+
+  // ---- join the warps, a warp an item: those that begin in warp b's span, or in the CTA before
+  // (b == -1), and go on
+  if (tid == 0) desc[blockIdx.x].seq = -1;
+  __syncthreads();
+#pragma unroll 1
+  for (int b = warp - 1; b < kWarps; b += kWarps) {
+    if (!(b < 0 ? sm.part[0] & 1 : sm.part[b] & 4)) continue;
+    int last = b;  // last warp with a part
+    bool ends = false;
+    for (int w = b + 1; w < kWarps && !ends; ++w)
+      if (sm.part[w] & 1) {
+        last = w;
+        ends = sm.part[w] & 2;
+      } else if (!(sm.part[w] & 8)) {
+        break;
+      }
+    const Place x = b < 0 ? sm.place[0][0] : sm.place[1][b];
+    const bool full = b >= 0 && ends;
+    if (b >= 0 && !ends && lane == 0)
+      desc[blockIdx.x] = Desc{x.seq, x.item, static_cast<int>((sm.lo + x.end - 1) / sm.quota), 0};
+    const float *tail = b < 0 ? nullptr : reinterpret_cast<const float *>(sm.ring[b]);
+    float *part = slots() + (2 * static_cast<size_t>(blockIdx.x) + (b < 0 ? 0 : 1)) * slot_floats(D);
+#pragma unroll 1
+    for (int e = lane; e < x.rows * (D / 4); e += 32) {
       const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-      if (row_first + r >= rows_all) continue;
-      float mx = sm.m[0][r];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm.m[w][r]);
+      float mx = b < 0 ? kNegBig : sm.m[1][b][r];
+      for (int w = b + 1; w <= last; ++w)
+        if (sm.part[w] & 1) mx = fmaxf(mx, sm.m[0][w][r]);
       float sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(sm.m[w][r] - mx);
-        const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][r][d]);
-        sum = fmaf(f, sm.l[w][r], sum);
-        acc.x = fmaf(f, x.x, acc.x);
-        acc.y = fmaf(f, x.y, acc.y);
-        acc.z = fmaf(f, x.z, acc.z);
-        acc.w = fmaf(f, x.w, acc.w);
-      }
-      if (begins && ends) {
+      auto add = [&](const float4 &o, float mw, float lw) {
+        const float f = ex2(mw - mx);
+        sum = fmaf(f, lw, sum);
+        acc.x = fmaf(f, o.x, acc.x);
+        acc.y = fmaf(f, o.y, acc.y);
+        acc.z = fmaf(f, o.z, acc.z);
+        acc.w = fmaf(f, o.w, acc.w);
+      };
+      if (b >= 0) add(*reinterpret_cast<const float4 *>(tail + r * S::OROW + d), sm.m[1][b][r], sm.l[1][b][r]);
+      for (int w = b + 1; w <= last; ++w)
+        if (sm.part[w] & 1) add(*reinterpret_cast<const float4 *>(heads() + w * (R * D) + r * D + d), sm.m[0][w][r], sm.l[0][w][r]);
+      if (full) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int rr = row_first + r, qi = rr / a.group;
-        T *op = static_cast<T *>(a.out) + (cur.q.row0 + static_cast<int64_t>(qi)) * a.o_row +
-                (static_cast<int64_t>(head) * a.group + (rr - qi * a.group)) * a.o_head + d;
+        const int rr = x.row_first + r, qi = rr / a.group;
+        T *op = static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
+                (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head + d;
         using X = Kv4Type<T>;
         uint2 v;
         v.x = kv4_bits<uint32_t>(X::from2(acc.x * inv, acc.y * inv));
@@ -605,21 +719,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         }
       }
     }
-    __syncthreads();
-    if (tid == 0 && seg_end == mylen) {
-      Desc x{-1, 0, 0, 0};
-      if (begins && !ends) {
-        const long long end = lo + cur.start + cur.q.n_rec;
-        x = Desc{cur.seq, cur.item, static_cast<int>((end - 1) / quota), 0};
-      }
-      desc[blockIdx.x] = x;
-    }
-    pos = seg_end;
   }
   // after a wait that ran out, do not leave while copies may still land here
   if (dead)
-    for (uint32_t i = used > SLOTS ? used - SLOTS : 0; i < issued; ++i)
-      mbar_wait(&sm.full[warp][i % SLOTS], (i / SLOTS) & 1, kWaitNs / 16);
+    for (int n = max(w1 - w0 - SLOTS, 0); n < w1 - w0; ++n)
+      mbar_wait(&sm.full[warp][n % SLOTS], n / SLOTS & 1, kWaitNs / 16);
 }
 
 // Joins the parts of the item that starts in part blockIdx.x and ends later.
@@ -669,7 +773,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Kv4AttnArgs a)
 
 template <typename T, int D, int NT>
 cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
-  constexpr int SLOTS = NT == 1 ? 4 : 6;
+  constexpr int SLOTS = D == 64 ? 5 : NT == 1 ? 3 : 5;  // units in flight: two CTAs fit an SM, or one with 16 rows
   auto kernel = kv4_attn_kernel<T, D, NT, SLOTS>;
   const int smem = static_cast<int>(sizeof(Smem<D, NT, SLOTS>));
   static std::atomic<uint64_t> done{0};
@@ -701,7 +805,9 @@ cudaError_t pick(const Kv4AttnArgs &a, cudaStream_t stream) {
 
 size_t kv4_step_workspace(int d, int num_sms) {
   const size_t ctas = 2 * static_cast<size_t>(num_sms);
-  return ctas * sizeof(Desc) + ctas * 2 * slot_floats(d) * sizeof(float);
+  // an item's first and last part of each CTA, and 8 rows that each warp leaves for its CTA (or half
+  // the CTAs with 16)
+  return ctas * sizeof(Desc) + ctas * 2 * slot_floats(d) * sizeof(float) + ctas * kWarps * 8 * d * sizeof(float);
 }
 
 cudaError_t launch_kv4_attn(Kv4AttnArgs a, cudaStream_t stream) {
