@@ -13,6 +13,7 @@ cache is :class:`KV4Cache` with :func:`kv4_append`, :func:`kv4_read` and
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -420,21 +421,23 @@ class KV4Cache:
 
     def __init__(self, pages, page_size: int, head_dim: int, dtype=None):
         import torch
-        dtype = torch.float16 if dtype is None else dtype
-        if dtype not in (torch.float16, torch.bfloat16):
+        if dtype is None or dtype is torch.float16:
+            dtype, code = torch.float16, MIXQ_KV4_F16
+        elif dtype is torch.bfloat16:
+            code = MIXQ_KV4_BF16
+        else:
             raise MixqError(1, f"cache dtype {dtype} must be torch.float16 or torch.bfloat16")
-        if pages.dtype != torch.uint8 or pages.dim() != 3:
+        if pages.dtype is not torch.uint8 or pages.dim() != 3:
             raise MixqError(1, "pages must be a uint8 tensor [n_pages, n_kv_heads, page bytes]")
         per = page_size * (head_dim + 8)
-        if pages.shape[2] != per or (pages.numel() and (
-                pages.stride(2) != 1 or (pages.shape[1] > 1 and pages.stride(1) != per))):
+        (n, heads, size), (stride, by_head, by_byte) = pages.shape, pages.stride()
+        if size != per or (n * heads * size and (by_byte != 1 or (heads > 1 and by_head != per))):
             raise MixqError(1, f"a kv head's part of a page must be {per} contiguous bytes, the "
                                "heads of a page one after another")
         self.pages, self.page_size, self.head_dim, self.dtype = pages, page_size, head_dim, dtype
-        self.n_kv_heads = pages.shape[1]
-        stride = pages.stride(0) if pages.shape[0] > 1 else max(1, pages.shape[1]) * per
-        self._desc = _KV4Desc(pages.data_ptr(), stride, pages.shape[0], page_size, pages.shape[1],
-                              head_dim, MIXQ_KV4_F16 if dtype == torch.float16 else MIXQ_KV4_BF16)
+        self.n_kv_heads, self.device = heads, pages.device
+        self._desc = _KV4Desc(pages.data_ptr(), stride if n > 1 else max(1, heads) * per, n,
+                              page_size, heads, head_dim, code)
         self._ref = ctypes.addressof(self._desc)
 
     @classmethod
@@ -447,71 +450,72 @@ class KV4Cache:
         return cls(pages, page_size, head_dim, dtype)
 
 
-def _kv4_rows(cache: KV4Cache, name: str, t, heads=None):
-    if t.dtype != cache.dtype or t.dim() != 3 or t.shape[2] != cache.head_dim or (
-            heads is not None and t.shape[1] != heads):
+def _kv4_rows(cache: KV4Cache, name: str, t, heads=None, rows=None):
+    """Checked (rows, heads, row stride, head stride) of a [rows, heads, head_dim] tensor; strides
+    of a dimension of one say nothing and are set."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not cache.dtype or len(shape) != 3 or shape[2] != cache.head_dim or (
+            heads is not None and shape[1] != heads):
         raise MixqError(1, f"{name} must be {cache.dtype} [rows, "
                            f"{'heads' if heads is None else heads}, {cache.head_dim}], not "
-                           f"{t.dtype} {tuple(t.shape)}")
-    if t.numel() and t.stride(2) != 1:
+                           f"{t.dtype} {tuple(shape)}")
+    n, h, d = shape
+    if rows is not None and n != rows:
+        raise MixqError(1, f"{name} must have {rows} rows")
+    if stride[2] != 1 and n * h * d:
         raise MixqError(1, f"the last dimension of {name} must be contiguous")
-    if t.device != cache.pages.device:
-        raise MixqError(1, f"{name} is on {t.device}, the cache on {cache.pages.device}")
-
-
-def _kv4_strides(t):
-    """(row, head) strides; those of a dimension of one say nothing and are set."""
-    head = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    return (t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1]) * head), head
+    if t.device != cache.device:
+        raise MixqError(1, f"{name} is on {t.device}, the cache on {cache.device}")
+    head = stride[1] if h > 1 else d
+    return n, h, stride[0] if n > 1 else max(1, h) * head, head
 
 
 def _kv4_ints(cache: KV4Cache, name: str, t, shape):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or (t.numel() > 1 and t.stride(-1) != 1):
+    if t.dtype is not torch.int32 or tuple(t.shape) != shape or (t.stride(-1) != 1 and t.numel() > 1):
         raise MixqError(1, f"{name} must be contiguous int32 {list(shape)}")
-    if t.device != cache.pages.device:
-        raise MixqError(1, f"{name} is on {t.device}, the cache on {cache.pages.device}")
+    if t.device != cache.device:
+        raise MixqError(1, f"{name} is on {t.device}, the cache on {cache.device}")
+    return t.data_ptr()
 
 
-def _kv4_batch(cache: KV4Cache, table, per_seq, cu, rows: int):
-    """Checked (n_seqs, rows, table, width, stride) of a call's batch."""
+def _kv4_batch(cache: KV4Cache, table, name: str, per_seq, cu, rows: int):
+    """Checked (n_seqs, rows, table, width, stride, per_seq, cu) of a call's batch; the last two may
+    be None."""
     if table.dim() != 2:
         raise MixqError(1, "the block table must be int32 [n_seqs, width]")
     n, width = table.shape
-    _kv4_ints(cache, "the block table", table, (n, width))
-    for name, t in per_seq:
-        _kv4_ints(cache, name, t, (n,))
+    at = _kv4_ints(cache, "the block table", table, (n, width))
+    if per_seq is not None:
+        per_seq = _kv4_ints(cache, name, per_seq, (n,))
     if cu is not None:
-        _kv4_ints(cache, "the row offsets", cu, (n + 1,))
+        cu = _kv4_ints(cache, "the row offsets", cu, (n + 1,))
     elif rows != n:
         raise MixqError(1, f"without row offsets there must be one row per sequence, not {rows} "
                            f"rows for {n} sequences")
-    return n, rows, table.data_ptr(), width, max(table.stride(0), width) if n > 1 else width
+    return n, rows, at, width, max(table.stride(0), width) if n > 1 else width, per_seq, cu
 
 
-class _On:
+_NOW = contextlib.nullcontext()
+
+
+def _on(cache: KV4Cache, stream):
     """The cache's device current, and `stream` (if given) the current stream, for a call."""
+    import torch
+    device = cache.device
+    if device.type != "cuda":
+        raise MixqError(6, "the cache must be on an sm_100 GPU")
+    if stream is None:
+        return _NOW if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise MixqError(1, f"the stream is on {stream.device}, the cache on {device}")
+    return torch.cuda.stream(stream)  # makes its device current too
 
-    def __init__(self, cache: KV4Cache, stream):
-        import torch
-        if not cache.pages.is_cuda:
-            raise MixqError(6, "the cache must be on an sm_100 GPU")
-        self.todo = []
-        if cache.pages.device.index != torch.cuda.current_device():
-            self.todo.append(torch.cuda.device(cache.pages.device))
-        if stream is not None:
-            if stream.device != cache.pages.device:
-                raise MixqError(1, f"the stream is on {stream.device}, the cache on "
-                                   f"{cache.pages.device}")
-            self.todo.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        for c in self.todo:
-            c.__enter__()
-
-    def __exit__(self, *e):
-        for c in reversed(self.todo):
-            c.__exit__(*e)
+def _current_stream(cache: KV4Cache) -> int:
+    import torch
+    # what torch.cuda.current_stream(device).cuda_stream says, without the object around it
+    return torch._C._cuda_getCurrentRawStream(cache.device.index)
 
 
 def kv4_append(k, v, cache: KV4Cache, table, seq_lens, cu_new=None, status=None,
@@ -521,15 +525,14 @@ def kv4_append(k, v, cache: KV4Cache, table, seq_lens, cu_new=None, status=None,
     table int32 [n_seqs, width]: pages of each sequence; seq_lens int32 [n_seqs]: lengths with
     the new rows; cu_new int32 [n_seqs + 1]: row offsets of the sequences (None: a row each).
     Strides are free but for the last dimension (k and v may be parts of one projection)."""
-    _kv4_rows(cache, "k", k, cache.n_kv_heads)
-    _kv4_rows(cache, "v", v, cache.n_kv_heads)
-    if v.shape[0] != k.shape[0]:
-        raise MixqError(1, f"k has {k.shape[0]} rows, v {v.shape[0]}")
-    b = _kv4_batch(cache, table, (("seq_lens", seq_lens),), cu_new, k.shape[0])
-    with _On(cache, stream):
-        _check(lib().mixq_kv4_append(cache._ref, k.data_ptr(), *_kv4_strides(k), v.data_ptr(),
-                                     *_kv4_strides(v), *b,
-                                     seq_lens.data_ptr(), _ptr(cu_new), _ptr(status), _stream()))
+    rows, _, k_row, k_head = _kv4_rows(cache, "k", k, cache.n_kv_heads)
+    v_rows, _, v_row, v_head = _kv4_rows(cache, "v", v, cache.n_kv_heads)
+    if v_rows != rows:
+        raise MixqError(1, f"k has {rows} rows, v {v_rows}")
+    b = _kv4_batch(cache, table, "seq_lens", seq_lens, cu_new, rows)
+    with _on(cache, stream):
+        _check(lib().mixq_kv4_append(cache._ref, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row,
+                                     v_head, *b, _ptr(status), _current_stream(cache)))
 
 
 def kv4_read(cache: KV4Cache, table, cu_rows, rows: int, first=None, k_out=None, v_out=None,
@@ -539,17 +542,17 @@ def kv4_read(cache: KV4Cache, table, cu_rows, rows: int, first=None, k_out=None,
     Row cu_rows[s] + i is position first[s] + i of sequence s (first None: from 0; cu_rows None:
     a row each); rows is the number of output rows."""
     import torch
-    shape = (rows, cache.n_kv_heads, cache.head_dim)
-    b = _kv4_batch(cache, table, () if first is None else (("first", first),), cu_rows, rows)
-    with _On(cache, stream):
-        k_out = torch.empty(shape, dtype=cache.dtype, device=cache.pages.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=cache.dtype, device=cache.pages.device) if v_out is None else v_out
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
-            _kv4_rows(cache, name, t, cache.n_kv_heads)
-            if t.shape[0] != rows:
-                raise MixqError(1, f"{name} must have {rows} rows")
-        _check(lib().mixq_kv4_read(cache._ref, k_out.data_ptr(), *_kv4_strides(k_out),
-                                   v_out.data_ptr(), *_kv4_strides(v_out), *b, _ptr(first), _ptr(cu_rows), _ptr(status), _stream()))
+    heads = cache.n_kv_heads
+    b = _kv4_batch(cache, table, "first", first, cu_rows, rows)
+    with _on(cache, stream):
+        if k_out is None:
+            k_out = torch.empty((rows, heads, cache.head_dim), dtype=cache.dtype, device=cache.device)
+        _, _, k_row, k_head = _kv4_rows(cache, "k_out", k_out, heads, rows)
+        if v_out is None:
+            v_out = torch.empty_like(k_out, memory_format=torch.contiguous_format)
+        _, _, v_row, v_head = _kv4_rows(cache, "v_out", v_out, heads, rows)
+        _check(lib().mixq_kv4_read(cache._ref, k_out.data_ptr(), k_row, k_head, v_out.data_ptr(),
+                                   v_row, v_head, *b, _ptr(status), _current_stream(cache)))
     return k_out, v_out
 
 
@@ -562,14 +565,13 @@ def kv4_workspace(cache: KV4Cache, max_rows: int = 0):
 
     max_rows: a bound on new tokens times n_q_heads / n_kv_heads of one sequence (0: none)."""
     import torch
-    dev = cache.pages.device
-    key = (dev.index, cache.head_dim, not 0 < max_rows <= _KV4_STEP_ROWS)
+    key = (cache.device.index, cache.head_dim, not 0 < max_rows <= _KV4_STEP_ROWS)
     n = _kv4_work_bytes.get(key)
     if n is None:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(cache.device):
             n = lib().mixq_kv4_attention_workspace_size(cache.head_dim, max_rows, 0)
         _kv4_work_bytes[key] = n
-    return torch.empty(n, dtype=torch.uint8, device=dev)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def kv4_attention(q, cache: KV4Cache, table, seq_lens, cu_new=None, max_new: int = 0, scale=None,
@@ -582,24 +584,23 @@ def kv4_attention(q, cache: KV4Cache, table, seq_lens, cu_new=None, max_new: int
     scratch from kv4_workspace (default: allocated for the call).  Returns out [rows,
     n_q_heads, head_dim]; a row that sees no key is zeros."""
     import torch
-    _kv4_rows(cache, "q", q)
-    b = _kv4_batch(cache, table, (("seq_lens", seq_lens),), cu_new, q.shape[0])
-    with _On(cache, stream):
+    rows, heads, q_row, q_head = _kv4_rows(cache, "q", q)
+    n, _, at, width, table_row, lens, cu = _kv4_batch(cache, table, "seq_lens", seq_lens, cu_new, rows)
+    with _on(cache, stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            o_head = cache.head_dim
+            o_row = max(1, heads) * o_head
         else:
-            _kv4_rows(cache, "out", out, q.shape[1])
-            if out.shape[0] != q.shape[0]:
-                raise MixqError(1, f"out must have {q.shape[0]} rows")
+            _, _, o_row, o_head = _kv4_rows(cache, "out", out, heads, rows)
         if work is None:
-            bound = 1 if cu_new is None else min(max_new, q.shape[0]) if max_new > 0 else q.shape[0]
-            work = kv4_workspace(cache, bound * q.shape[1] // max(1, cache.n_kv_heads))
-        elif work.device != cache.pages.device or not work.is_contiguous():
+            bound = 1 if cu is None else min(max_new, rows) if max_new > 0 else rows
+            work = kv4_workspace(cache, bound * heads // max(1, cache.n_kv_heads))
+        elif work.device != cache.device or not work.is_contiguous():
             raise MixqError(1, "work must be contiguous and on the cache's device")
-        n, rows, tptr, width, tstride = b
         _check(lib().mixq_kv4_attention(
-            cache._ref, q.data_ptr(), *_kv4_strides(q), out.data_ptr(), *_kv4_strides(out), q.shape[1], n, rows, max_new, tptr, width, tstride,
-            seq_lens.data_ptr(), _ptr(cu_new),
+            cache._ref, q.data_ptr(), q_row, q_head, out.data_ptr(), o_row, o_head, heads, n, rows,
+            max_new, at, width, table_row, lens, cu,
             cache.head_dim ** -0.5 if scale is None else float(scale), window, sinks,
-            work.data_ptr(), work.numel() * work.element_size(), _ptr(status), _stream()))
+            work.data_ptr(), work.nbytes, _ptr(status), _current_stream(cache)))
     return out
