@@ -103,9 +103,26 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
 // Token that byte i of a V word of quad t belongs to.
 __device__ __forceinline__ int quad_token(int t, int i) { return 2 * t + (i >> 1) + 8 * (i & 1); }
 
-// The eight codes of a lane (one row spread over LANES lanes) as nibbles
-// 0..7 = elements 0..7, and the row's (s, lo) pair.
-template <typename T, int LANES>
+// x / 15, rounded to nearest: the quotient from the rounded reciprocal, corrected once with
+// its exact remainder (P. Markstein, IBM J. Res. Dev. 34, 1990).  x is 0 or the difference of
+// two 16-bit values, so nothing here underflows inexactly.
+__device__ __forceinline__ float div15(float x) {
+  constexpr float r = 1.f / 15.f;
+  const float q = __fmul_rn(x, r);
+  return __fmaf_rn(__fmaf_rn(-15.f, q, x), r, q);
+}
+
+// 1 / s, rounded to nearest, for a normal s with an 11-bit significand whose reciprocal is
+// normal: one such correction (same source) of an approximation within a unit in the last place.
+__device__ __forceinline__ float reciprocal(float s) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  return __fmaf_rn(__fmaf_rn(-s, y, 1.f), y, y);
+}
+
+// The eight codes of a lane (one row spread over LANES lanes) as a word, and the row's (s, lo)
+// pair.  K: nibble p = dim 2p, nibble p + 4 = dim 2p + 1; else nibbles 0..7 = dims 0..7.
+template <typename T, int LANES, bool K>
 __device__ __forceinline__ uint32_t quantize8(const uint4 &raw, uint32_t *pair) {
   using X = Kv4Type<T>;
   using T2 = typename X::T2;
@@ -124,38 +141,40 @@ __device__ __forceinline__ uint32_t quantize8(const uint4 &raw, uint32_t *pair) 
   const float2 ends = X::f2(e);
   const float lo = ends.x, hi = -ends.y;
   const float range = __fsub_rn(hi, lo);
-  const T2 sl = X::from2(__fdiv_rn(range, 15.f), lo);
+  const T2 sl = X::from2(div15(range), lo);
   float s = X::f2(sl).x;
   if (s < 1.17549435e-38f) s = 0.f;  // a bf16 subnormal's reciprocal may not be finite
   const bool finite = range - range == 0.f;  // neither end NaN or infinite, nor their distance
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t codes = 0;
+  const float inv = s > 0.f ? reciprocal(s) : 0.f;
+  // 1.5 * 2^23 + (x - lo) * inv, each step rounded once: the last rounds half to even and leaves
+  // the code in the low bits
+  const uint64_t nlo = f32x2(-lo, -lo), inv2 = f32x2(inv, inv);
+  uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = X::f2(x[i]);
-    const float u = fminf(__fmul_rn(__fsub_rn(f.x, lo), inv), 15.f);
-    const float w = fminf(__fmul_rn(__fsub_rn(f.y, lo), inv), 15.f);
-    // 1.5 * 2^23 + u: round half to even, code in the low bits
-    codes |= (__float_as_uint(__fadd_rn(u, 12582912.f)) & 15u) << (8 * i);
-    codes |= (__float_as_uint(__fadd_rn(w, 12582912.f)) & 15u) << (8 * i + 4);
+    const float2 u = from_f32x2(mul_f32x2(add_f32x2(f32x2(f.x, f.y), nlo), inv2));
+    // one at a time: ptxas joins the packed product and sum into one rounding
+    c[2 * i] = __float_as_uint(__fadd_rn(u.x, 12582912.f));
+    c[2 * i + 1] = __float_as_uint(__fadd_rn(u.y, 12582912.f));
+  }
+  // s is range / 15 to within a small part unless it is subnormal in T; only then can a code pass 15
+  if (__builtin_expect(__any_sync(0xffffffffu, __fmul_rn(range, inv) >= 15.5f), 0)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = min(c[i], 0x4b40000fu);
+  }
+  // c[i] = 0x4b400000 + code: codes times their places add up, and the constant parts in one word
+  constexpr uint32_t kBits = 0x4b400000u;
+  uint32_t w;
+  if (K) {
+    const uint32_t even = c[0] + c[2] * 16 + c[4] * 256 + c[6] * 4096, odd = c[1] + c[3] * 16 + c[5] * 256 + c[7] * 4096;
+    w = even + odd * 65536 - kBits * 0x1111u * 0x10001u;
+  } else {
+    w = c[0] + c[1] * 16 + c[2] * 256 + c[3] * 4096 + (c[4] + c[5] * 16 + c[6] * 256 + c[7] * 4096) * 65536 -
+        kBits * 0x11111111u;
   }
   *pair = finite ? kv4_bits<uint32_t>(X::from2(s, lo)) : 0x7fff7fffu;
-  return codes;
-}
-
-// Nibbles 0..7 = dims 0..7 -> K word (nibble p = dim 2p, nibble p + 4 = dim 2p + 1).
-__device__ __forceinline__ uint32_t k_word(uint32_t c) {
-  uint32_t even = c & 0x0f0f0f0fu, odd = (c >> 4) & 0x0f0f0f0fu;
-  even = (even | (even >> 4)) & 0x00ff00ffu;
-  odd = (odd | (odd >> 4)) & 0x00ff00ffu;
-  return __byte_perm(even, odd, 0x6420);
-}
-
-__device__ __forceinline__ uint32_t k_unword(uint32_t w) {
-  uint32_t even = __byte_perm(w, 0, 0x4140), odd = __byte_perm(w, 0, 0x4342);
-  even = (even | (even << 4)) & 0x0f0f0f0fu;
-  odd = (odd | (odd << 4)) & 0x0f0f0f0fu;
-  return even | (odd << 4);
+  return w;
 }
 
 template <typename T, int D>
@@ -196,11 +215,11 @@ __global__ void __launch_bounds__(kWarps * 32)
       const int tok = quad_token(t, i);
       const bool in = tok >= p.t0 && tok < p.t1;
       uint32_t kp, vp;
-      const uint32_t kc = quantize8<T, LANES>(kr[i], &kp);
-      vw[i] = quantize8<T, LANES>(vr[i], &vp);
+      const uint32_t kc = quantize8<T, LANES, true>(kr[i], &kp);
+      vw[i] = quantize8<T, LANES, false>(vr[i], &vp);
       if (in) {
         valid |= 1 << i;
-        reinterpret_cast<uint32_t *>(rec + tok * (D / 2))[l] = k_word(kc);
+        reinterpret_cast<uint32_t *>(rec + tok * (D / 2))[l] = kc;
         if (l == 0) {
           reinterpret_cast<uint32_t *>(rec + 16 * D)[tok] = kp;
           reinterpret_cast<uint32_t *>(rec + 16 * D + 64)[tok] = vp;
@@ -222,22 +241,32 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// Eight codes (nibbles 0..7) and the row's pair -> eight values of T.
-template <typename T>
-__device__ __forceinline__ uint4 dequantize8(uint32_t c, float2 sl) {
+// A word of eight codes and the row's pair -> eight values of T (word orders as in quantize8).
+template <typename T, bool K>
+__device__ __forceinline__ uint4 dequantize8(uint32_t w, float2 sl) {
   using X = Kv4Type<T>;
+  // 2^23 + code * 16^p as bits, exact, for the four nibbles of a half; c * s is exact, so the sum
+  // rounds once (s / 16^p is exact as well: s has 11 bits and is normal, or 0, in fp32)
+  const uint64_t s01 = f32x2(sl.x, sl.x * 0.0625f), s23 = f32x2(sl.x * 0.00390625f, sl.x * 0.000244140625f),
+                 lo = f32x2(sl.y, sl.y), down = f32x2(-8388608.f, -8388608.f);
+  float v[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t u = h ? w >> 16 : w;
+    const uint64_t a = f32x2(__uint_as_float(0x4b000000u | (u & 0xfu)), __uint_as_float(0x4b000000u | (u & 0xf0u)));
+    const uint64_t b = f32x2(__uint_as_float(0x4b000000u | (u & 0xf00u)), __uint_as_float(0x4b000000u | (u & 0xf000u)));
+    const float2 x = from_f32x2(fma_f32x2(add_f32x2(a, down), s01, lo)), y = from_f32x2(fma_f32x2(add_f32x2(b, down), s23, lo));
+    v[K ? h : 4 * h] = x.x, v[K ? 2 + h : 4 * h + 1] = x.y;
+    v[K ? 4 + h : 4 * h + 2] = y.x, v[K ? 6 + h : 4 * h + 3] = y.y;
+  }
+  // s was rounded, so 15 s + lo can pass the type's largest value: hold it there (NaN passes)
+  if (__builtin_expect(fmaf(15.f, sl.x, sl.y) > X::max_finite, 0)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] > X::max_finite ? X::max_finite : v[i];
+  }
   uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // 2^23 + code as bits, exact; c * s is exact, so the sum rounds once
-    const float a = __uint_as_float(0x4b000000u | ((c >> (8 * i)) & 15u)) - 8388608.f;
-    const float b = __uint_as_float(0x4b000000u | ((c >> (8 * i + 4)) & 15u)) - 8388608.f;
-    float x = fmaf(a, sl.x, sl.y), y = fmaf(b, sl.x, sl.y);
-    // s was rounded, so 15 s + lo can pass the type's largest value: hold it there (NaN passes)
-    x = x > X::max_finite ? X::max_finite : x;
-    y = y > X::max_finite ? X::max_finite : y;
-    o[i] = kv4_bits<uint32_t>(X::from2(x, y));
-  }
+  for (int i = 0; i < 4; ++i) o[i] = kv4_bits<uint32_t>(X::from2(v[2 * i], v[2 * i + 1]));
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -281,9 +310,9 @@ __global__ void __launch_bounds__(kWarps * 32)
       if (tok < p.t0 || tok >= p.t1) continue;
       const int64_t row = p.row0 + tok;
       *reinterpret_cast<uint4 *>(k + row * r.k_row) =
-          dequantize8<T>(k_unword(kw[it][i]), kv4_pair<BF>(kp[it][i]));
+          dequantize8<T, true>(kw[it][i], kv4_pair<BF>(kp[it][i]));
       *reinterpret_cast<uint4 *>(v + row * r.v_row) =
-          dequantize8<T>(vw[it][i], kv4_pair<BF>(vp[it][i]));
+          dequantize8<T, false>(vw[it][i], kv4_pair<BF>(vp[it][i]));
     }
   }
 }

@@ -78,31 +78,6 @@ struct TileSmem {
   int dead;
 };
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t a) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a));
-  return f;
-}
 __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -430,10 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = X::f2(kv4_bits<T2>(u[e]));
-          sum = add2(sum, pack2(f.x, f.y));
+          sum = add_f32x2(sum, f32x2(f.x, f.y));
         }
       }
-      const float2 f = unpack2(sum);
+      const float2 f = from_f32x2(sum);
       qsum = f.x + f.y;
     };
     wait(&sm.item_full[0], 0, &sm.dead, a.status);
@@ -447,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       const int n = x.n;
       if (n == 0 || sm.dead) break;
       const bool active = i * 128 < x.rows;
-      uint64_t la = pack2(0.f, 0.f), lb = la;
+      uint64_t la = f32x2(0.f, 0.f), lb = la;
       float base = 0.f;         // what is added to t: 6 - m, m a whole number, once a key was seen
       float limit = -INFINITY;  // t + base above this moves the maximum
       if (active) {
@@ -458,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         const int wlo = valid && a.window > 0 ? max(max(x.pos0 + qi, 0) - a.window + 1, 0) : 0;
         const int tmin = min(x.pos0 + (x.first + i * 128) / a.group + 1, x.len);
         const int tmax = max(x.pos0 + (x.first + min(i * 128 + 128, x.rows) - 1) / a.group, 0);
-        const uint64_t qs2 = pack2(qsum, qsum);
+        const uint64_t qs2 = f32x2(qsum, qsum);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int k0 = (t0 + j + (t0 + j >= sinks ? skip : 0)) * kKeys, st = (jt + j) & 3;
@@ -480,11 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           } buf[2];
           // t + base of 32 keys in place of their scores, and the largest
           auto scores = [&](Chunk &t, int c) -> float {
-            const uint64_t b2 = pack2(base, base);
+            const uint64_t b2 = f32x2(base, base);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float4 x = kp[c * 16 + e];
-              t.d[e] = fma2(t.d[e], pack2(x.x, x.y), fma2(pack2(x.z, x.w), qs2, b2));
+              t.d[e] = fma_f32x2(t.d[e], f32x2(x.x, x.y), fma_f32x2(f32x2(x.z, x.w), qs2, b2));
             }
             if (__builtin_expect(!whole, 0)) {
               // one bit per key, so that no lane branches
@@ -511,11 +486,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             const float al = limit > -INFINITY ? ex2f(d) : 1.f;  // a power of two; nothing to scale before the first key
             if (need) limit = 14.f;
             base += d;
-            const uint64_t d2 = pack2(d, d), al2 = pack2(al, al);
+            const uint64_t d2 = f32x2(d, d), al2 = f32x2(al, al);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) t.d[e] = add2(t.d[e], d2);
-            la = mul2(la, al2);
-            lb = mul2(lb, al2);
+            for (int e = 0; e < 16; ++e) t.d[e] = add_f32x2(t.d[e], d2);
+            la = mul_f32x2(la, al2);
+            lb = mul_f32x2(lb, al2);
             if (j > 0) {
               wait(&sm.o_full[i], (jn + j - 1) & 1, &sm.dead, a.status);
               tc_fence_after();
@@ -565,10 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
               uint32_t p[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const float2 x = unpack2(t.d[e]);
+                const float2 x = from_f32x2(t.d[e]);
                 const float p0 = ex2f(x.x), p1 = ex2f(x.y);
-                if (e & 1) lb = add2(lb, pack2(p0, p1));
-                else la = add2(la, pack2(p0, p1));
+                if (e & 1) lb = add_f32x2(lb, f32x2(p0, p1));
+                else la = add_f32x2(la, f32x2(p0, p1));
                 p[e] = kv4_bits<uint32_t>(X::from2(p0, p1));
               }
               if (next) mx = scores(buf[h ^ 1], c + 1);
@@ -590,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       if (nx.n > 0) have_q(nx);
       // ---- the result.  Column c of O is dim 2c, column D/2 + c dim 2c + 1.
       if (active) {
-        const float2 l0 = unpack2(la), l1 = unpack2(lb);
+        const float2 l0 = from_f32x2(la), l1 = from_f32x2(lb);
         const float sum = (l0.x + l0.y) + (l1.x + l1.y);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const bool valid = r < x.rows, begins = x.t0 == 0, full = begins && x.t0 + n == x.tiles;

@@ -150,6 +150,34 @@ def test_append_and_read_special_rows(dtype, D):
             assert torch.equal(torch.nan_to_num(a, nan=7.0), torch.nan_to_num(b, nan=7.0))
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_append_at_every_range(dtype):
+    """Rows from 0 to each positive value of the type: every quotient by 15 and every reciprocal of a scale that
+    rows can have, bit for bit."""
+    D = 64
+    top = torch.arange(1, 0x7C00 if dtype == F16 else 0x7F80, dtype=torch.int16).view(dtype)
+    g = torch.Generator().manual_seed(9)
+    part = torch.rand((len(top), D), generator=g)
+    part[:, 0], part[:, 1] = 0.0, 1.0
+    part[:, 2:18] = torch.arange(16) / 15.0 + 1 / 30  # near the borders between codes
+    x = (part.clamp(max=1.0) * top.float()[:, None]).to(dtype)
+    n = len(top)
+    cache = mq.KV4Cache.empty(-(-n // 128), 1, D, 128, dtype)
+    table = torch.arange(cache.pages.shape[0], dtype=torch.int32, device="cuda")[None]
+    mq.kv4_append(x[:, None].cuda(), x[:, None].flip(0).contiguous().cuda(), cache, table, ints([n]), ints([0, n]))
+    codes, s, lo = ref.quantize(x)
+    host = ref.Pages(cache.pages.cpu(), 128, D, dtype)
+    raw = host.p[:, 0].reshape(-1, 16 * (D + 8))[:-(-n // 16)]
+    tok, dim = torch.arange(16)[:, None], torch.arange(D)[None]
+    for place, at, flip in ((ref.k_place, 16 * D, False), (ref.v_place, 16 * D + 64, True)):
+        byte, shift = place(tok, dim, D)
+        got = (raw[:, byte].long() >> shift & 15).reshape(-1, D)[:n]
+        pair = raw[:, at:at + 64].contiguous().view(dtype).reshape(-1, 2)[:n]
+        want = (codes.flip(0), s.flip(0), lo.flip(0)) if flip else (codes, s, lo)
+        assert torch.equal(pair[:, :1], want[1]) and torch.equal(pair[:, 1:], want[2])
+        assert torch.equal(got, want[0]), f"{int((got != want[0]).sum())} codes differ"
+
+
 def test_append_leaves_out_negative_positions_and_bad_offsets():
     D, page, n_kv = 128, 16, 2
     pages, table, g = make(4, [20, 20, 20], n_kv, D, page, F16)
