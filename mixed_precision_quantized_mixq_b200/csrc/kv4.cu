@@ -47,13 +47,23 @@ __device__ __forceinline__ int find_seq(const Kv4Batch &b, int v, int lane) {
 struct Place {
   int row0;       // row of the record's token 0 (may lie before the range)
   int t0, t1;     // tokens [t0, t1) of the record belong to the call
-  uint8_t *rec;   // record of kv head 0
+  int page;       // of the record; not checked
+  int64_t off;    // of the record of kv head 0 in its page
 };
+
+// The record itself, null if its page is not usable.
+__device__ __forceinline__ uint8_t *record(const Kv4Cache &c, const Place &p, int lane, int32_t *status) {
+  if (p.page < 0 || p.page >= c.n_pages) {
+    if (lane == 0) record_error(status, kErrInvalidArg);
+    return nullptr;
+  }
+  return c.pages + p.page * c.page_stride + p.off;
+}
 
 // The record that virtual index v stands for, or t0 == t1.
 __device__ __forceinline__ Place locate(const Kv4Cache &c, const Kv4Batch &b, int v, int lane,
                                         bool append, int32_t *status) {
-  Place p{0, 0, 0, nullptr};
+  Place p{0, 0, 0, -1, 0};
   int s, local;
   if (b.cu) {
     s = find_seq(b, v, lane);
@@ -77,16 +87,11 @@ __device__ __forceinline__ Place locate(const Kv4Cache &c, const Kv4Batch &b, in
   const int64_t t1 = min(first + static_cast<int64_t>(n) - base, static_cast<int64_t>(16));
   if (t1 <= t0) return p;
   const int slot = rec / c.recs_per_page;
-  const int page = slot < b.table_width ? __ldg(b.table + s * b.table_stride + slot) : -1;
-  if (page < 0 || page >= c.n_pages) {
-    if (lane == 0) record_error(status, kErrInvalidArg);
-    return p;
-  }
+  p.page = slot < b.table_width ? __ldg(b.table + s * b.table_stride + slot) : -1;
   p.t0 = static_cast<int>(t0);
   p.t1 = static_cast<int>(t1);
   p.row0 = static_cast<int>(r.x + (base - first));
-  p.rec = c.pages + page * c.page_stride +
-          static_cast<int64_t>(rec - slot * c.recs_per_page) * kv4_rec_bytes(c.d);
+  p.off = static_cast<int64_t>(rec - slot * c.recs_per_page) * kv4_rec_bytes(c.d);
   return p;
 }
 
@@ -178,7 +183,7 @@ __device__ __forceinline__ uint32_t quantize8(const uint4 &raw, uint32_t *pair) 
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 4)
     kv4_append_kernel(Kv4Cache c, Kv4Batch b, Kv4Rows r, int32_t *status) {
   constexpr int LANES = D / 8, RPW = 32 / LANES;  // lanes per row, rows per warp load
   griddep_wait();
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const Place p = locate(c, b, blockIdx.x, lane, true, status);
   if (p.t0 >= p.t1) return;
   const int sub = lane / LANES, l = lane % LANES;
-  uint8_t *rec = p.rec + h * static_cast<int64_t>(c.recs_per_page) * kv4_rec_bytes(D);
+  uint8_t *rec = nullptr;
   const T *k = static_cast<const T *>(r.k) + h * r.k_head + l * 8;
   const T *v = static_cast<const T *>(r.v) + h * r.v_head + l * 8;
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -207,6 +212,11 @@ __global__ void __launch_bounds__(kWarps * 32)
       const int64_t row = p.row0 + tok;
       kr[i] = in ? __ldg(reinterpret_cast<const uint4 *>(k + row * r.k_row)) : zero;
       vr[i] = in ? __ldg(reinterpret_cast<const uint4 *>(v + row * r.v_row)) : zero;
+    }
+    if (it == 0) {  // only here, so that the page's look-up and the rows' loads overlap
+      rec = record(c, p, lane, status);
+      if (!rec) return;
+      rec += h * static_cast<int64_t>(c.recs_per_page) * kv4_rec_bytes(D);
     }
     uint32_t vw[4];
     int valid = 0;
@@ -283,7 +293,9 @@ __global__ void __launch_bounds__(kWarps * 32)
   const Place p = locate(c, b, blockIdx.x, lane, false, status);
   if (p.t0 >= p.t1) return;
   const int sub = lane / LANES, l = lane % LANES;
-  const uint8_t *rec = p.rec + h * static_cast<int64_t>(c.recs_per_page) * kv4_rec_bytes(D);
+  const uint8_t *rec = record(c, p, lane, status);
+  if (!rec) return;
+  rec += h * static_cast<int64_t>(c.recs_per_page) * kv4_rec_bytes(D);
   T *k = const_cast<T *>(static_cast<const T *>(r.k)) + h * r.k_head + l * 8;
   T *v = const_cast<T *>(static_cast<const T *>(r.v)) + h * r.v_head + l * 8;
   uint32_t kw[4 / RPW][4], vw[4 / RPW][4], kp[4 / RPW][4], vp[4 / RPW][4];
