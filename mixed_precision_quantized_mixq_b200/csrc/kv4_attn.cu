@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kv4.h"
 #include "ptx.cuh"
@@ -98,7 +99,7 @@ __device__ __forceinline__ int64_t seq_cost(const Seq &q, int n_kv) {
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -107,7 +108,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     }
     pre_i += 32 / kUnit;
   };
-  auto issue = [&](int n) {  // the span's n-th unit
-    const int u = n % (32 / kUnit), slot = n % SLOTS;
+  auto issue = [&](int n, int slot) {  // the span's n-th unit
+    const int u = n % (32 / kUnit);
     if (u == 0) {
       place = pre_off;
       if (pre_off >= 0) {
@@ -304,9 +305,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
   look_up();
 #pragma unroll 1
   for (int i = 0; i < SLOTS; ++i)
-    if (w0 + i < w1) issue(i);
+    if (w0 + i < w1) issue(i, i);
 
   bool dead = false;
+  int slot = 0;
+  uint32_t phase = 0;
   const float sl2 = a.scale * 1.4426950408889634f;
 
   int parts = w0 < w1 ? 0 : 8;
@@ -331,49 +334,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
       for (int w = 0; w < WORDS; ++w)
         raw[w] = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + w) : make_uint4(0, 0, 0, 0);
-      float sum = 0.f;
-      int e = 0;
-      if (BF) {
-        // bf16 rows go to fp16 under a power of two that puts the row's largest
-        // value into [2^13, 2^14): exact down to 2^-30 of it
-        float mx = 0.f;
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          const uint32_t u[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[i] << 16)),
-                                 fabsf(__uint_as_float(u[i] & 0xffff0000u))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-        e = max(-100, ex - 13);
-      }
-      const float down = BF ? pow2(-e) : 1.f;
+      // rows go to fp16 under a power of two that puts the row's largest value into [2^13, 2^14);
+      // dims whose codes are c * 2^-20 divided by 16, so that all products have one scale: exact
+      // down to 2^-24 of the largest
+      float2 f[WORDS][4];
+      float mx = 0.f, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < WORDS; ++w) {
         const uint32_t u[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x, y;
-          if (BF) {
-            x = __uint_as_float(u[i] << 16) * down;
-            y = __uint_as_float(u[i] & 0xffff0000u) * down;
-            qf[nt][w][i] = pack_half2(x, y);
-          } else {
-            const float2 f = __half22float2(kv4_bits<__half2>(u[i]));
-            x = f.x;
-            y = f.y;
-            qf[nt][w][i] = u[i];
-          }
+          f[w][i] = kv4_pair<BF>(u[i]);
+          mx = fmaxf(mx, fmaxf(fabsf(f[w][i].x), fabsf(f[w][i].y)));
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = max(-100, static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 13);
+      const float down = pow2(-e);
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = f[w][i].x * down, y = f[w][i].y * down;
+          qf[nt][w][i] = i & 1 ? pack_half2(x * 0.0625f, y * 0.0625f) : pack_half2(x, y);
           sum += x;
           sum += y;
         }
-      }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const float up = sl2 * (BF ? pow2(e) : 1.f);
+      const float up = sl2 * pow2(e);
       const float mycs = up * 16777216.f, myqs = up * sum;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -407,17 +397,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
       }
     }
 
+    // positions [from, to): units whose keys all rows see
+    const int to = cur.start + min(max(pmin + 1, 0), cur.q.len) / kUnitKeys - cur.q.skip_by;
+    const int from = a.window > 0 ? cur.start + max((max(edge_max, -1) + kUnitKeys) / kUnitKeys - cur.q.skip_by, cur.q.skip_at)
+                                  : cur.start;
+
     // ---- the warp's units of this segment
 #pragma unroll 1
     for (int i = pos; i < seg_end; ++i) {
-      const int slot = (i - w0) % SLOTS;
-      if (!dead && !mbar_wait(&sm.full[warp][slot], (i - w0) / SLOTS & 1, kWaitNs)) {
+      if (!dead && !mbar_wait(&sm.full[warp][slot], phase, kWaitNs)) {
         dead = true;
         if (lane == 0) record_error(a.status, kErrTimeout);
       }
       const int ok = dead ? 0 : sm.ok[warp][slot];
-      const int j0 = cur.unit(i) * kUnitKeys;
-      const bool none = !ok || j0 > pmax || (a.window > 0 && j0 + kUnitKeys <= edge_min + 1 && j0 >= a.sinks);
+      const bool whole = i >= from && i < to && ok == 3;
+      int j0 = 0;
+      bool none = false;
+      if (!whole) {
+        j0 = cur.unit(i) * kUnitKeys;
+        none = !ok || j0 > pmax || (a.window > 0 && j0 + kUnitKeys <= edge_min + 1 && j0 >= a.sinks);
+      }
       if (!none) {
         // scores, less the maxima, of tokens g and g + 8 of each record for columns 2t, 2t + 1
         float s[kUnit][NT][4], vs[kUnit][2], vl[kUnit][2];
@@ -444,25 +443,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
           vs[r][0] = v0.x, vs[r][1] = v1.x, vl[r][0] = v0.y, vl[r][1] = v1.y;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < WORDS; ++w) {
               const uint32_t a8 = ka[w] >> 8, b8 = kb[w] >> 8;
               mma16816(x, ka[w] & 0x000f000fu, kb[w] & 0x000f000fu, a8 & 0x000f000fu,
                        b8 & 0x000f000fu, qf[nt][w][0], qf[nt][w][2]);
-              mma16816(y, ka[w] & 0x00f000f0u, kb[w] & 0x00f000f0u, a8 & 0x00f000f0u,
+              mma16816(x, ka[w] & 0x00f000f0u, kb[w] & 0x00f000f0u, a8 & 0x00f000f0u,
                        b8 & 0x00f000f0u, qf[nt][w][1], qf[nt][w][3]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float2 k = j < 2 ? kp0 : kp1;
-              const float raw = fmaf(y[j], 0.0625f, x[j]);
-              s[r][nt][j] = fmaf(raw * k.x, cs[nt][j & 1], fmaf(k.y, qs[nt][j & 1], -m[nt][j & 1]));
+              s[r][nt][j] = fmaf(x[j] * k.x, cs[nt][j & 1], fmaf(k.y, qs[nt][j & 1], -m[nt][j & 1]));
             }
           }
         }
-        const bool whole = ok == 3 && j0 <= min(pmin + 1, cur.q.len) - kUnitKeys &&
-                           (a.window <= 0 || j0 > edge_max || j0 + kUnitKeys <= a.sinks);
         if (!whole) {
           const int last = min(pmax, cur.q.len - 1);
           // a column's row sees key j when j < vis and (j >= wlo or j < sinks); columns without a row
@@ -562,34 +558,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         }
 
         // ---- their sums, and the products with V
+        // a key hidden from this row must not reach it through 0 * NaN
+        auto products = [&](auto hides) {
+#pragma unroll
+          for (int r = 0; r < kUnit; ++r) {
+            const float s0 = vs[r][0] * sig, s1 = vs[r][1] * sig;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool hid = hides.value && s[r][nt][j] == -INFINITY;
+                z[nt][j & 1] = hid ? z[nt][j & 1] : fmaf(p[r][nt][j], vl[r][j / 2], z[nt][j & 1]);
+                p[r][nt][j] = hid ? 0.f : p[r][nt][j] * (j < 2 ? s0 : s1);
+              }
+          }
+        };
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          l[nt][0] += sum[nt][0];
+          l[nt][1] += sum[nt][1];
+        }
+        if (whole)
+          products(std::false_type{});
+        else
+          products(std::true_type{});
 #pragma unroll
         for (int r = 0; r < kUnit; ++r) {
           uint32_t p0[NT], p1[NT];
-          const float s0 = vs[r][0] * sig, s1 = vs[r][1] * sig;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float w[4];
-            if (whole) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                z[nt][j & 1] = fmaf(p[r][nt][j], vl[r][j / 2], z[nt][j & 1]);
-                w[j] = p[r][nt][j] * (j < 2 ? s0 : s1);
-              }
-            } else {
-              // a key hidden from this row must not reach it through 0 * NaN
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const bool hid = s[r][nt][j] == -INFINITY;
-                z[nt][j & 1] += hid ? 0.f : p[r][nt][j] * vl[r][j / 2];
-                w[j] = hid ? 0.f : p[r][nt][j] * (j < 2 ? s0 : s1);
-              }
-            }
-            if (r == 0) {
-              l[nt][0] += sum[nt][0];
-              l[nt][1] += sum[nt][1];
-            }
-            p0[nt] = transpose8x8(pack_half2(w[0], w[1]));
-            p1[nt] = transpose8x8(pack_half2(w[2], w[3]));
+            p0[nt] = transpose8x8(pack_half2(p[r][nt][0], p[r][nt][1]));
+            p1[nt] = transpose8x8(pack_half2(p[r][nt][2], p[r][nt][3]));
           }
           const uint8_t *rec = sm.ring[warp][slot][r];
 #pragma unroll
@@ -608,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         }
       }
       __syncwarp();
-      if (i + SLOTS < w1) issue(i + SLOTS - w0);
+      if (i + SLOTS < w1) issue(i + SLOTS - w0, slot);
+      if (++slot == SLOTS) slot = 0, phase ^= 1;
     }
 
     // ---- the segment's result.  Rows 8 i + g of the products are dims 2 (8 i + g) (x 2^-24) and
