@@ -58,6 +58,7 @@ struct Item {
   int n, t0, tiles, sinks, skip;  // tiles of the whole item; tile i is key tile i, from sinks on i + skip
   int row0, rows, len, pos0;      // rows: of this block
   int first, head;                // first row of the block within the sequence's rows
+  int n0;                         // tiles [t0, t0 + n0) concern the first row tile: n, or n - 1 where it sees no key of the last
 };
 
 template <int D>
@@ -67,6 +68,7 @@ struct TileSmem {
   alignas(1024) uint8_t v[2][kKeys * D * 2];
   alignas(16) float4 kp[4][kKeys / 2];  // per pair of keys: s0 s1 lo0 lo1, times scale log2(e)
   alignas(8) uint8_t hidden[4][8];  // records of the tile whose page is not usable
+  alignas(16) int4 sight[kRows];  // of a row: key j is seen when j < x and (j >= y or j < sinks); z, w: of its row tile
   Item item[kItems];
   int64_t src[2][32];  // records of four tiles: offset in the pages, -1 beyond the keys, -2 page not usable
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], par_full[4], s_full[2], p_full[2], o_full[2];
@@ -240,7 +242,9 @@ struct Walk {
 };
 
 struct Desc {  // item whose last part is not in the CTA that starts it
-  int seq, block, head, last;
+  int last;               // CTA of the last part, -1: no such item
+  int row0, first, rows;  // as in Item
+  int head, pad[3];
 };
 
 __host__ __device__ constexpr size_t slot_floats(int d) { return kRows * (static_cast<size_t>(d) + 2); }
@@ -419,29 +423,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 #pragma unroll 1
     for (int it = 0;; ++it) {
       const Item &x = sm.item[it % kItems], &nx = sm.item[(it + 1) % kItems];  // x has arrived already
-      const int n = x.n;
-      if (n == 0 || sm.dead) break;
+      if (x.n == 0 || sm.dead) break;
+      const int n = i ? x.n : x.n0;  // of this row tile
       const bool active = i * 128 < x.rows;
       uint64_t la = f32x2(0.f, 0.f), lb = la;
       float base = 0.f;         // what is added to t: 6 - m, m a whole number, once a key was seen
       float limit = -INFINITY;  // t + base above this moves the maximum
       if (active) {
-        const bool valid = r < x.rows;
-        const int qi = (x.first + r) / a.group, t0 = x.t0, sinks = x.sinks, skip = x.skip;
-        // key j is visible when j < vis and (j >= wlo or j < sinks)
-        const int vis = valid ? min(x.pos0 + qi + 1, x.len) : x.len;
-        const int wlo = valid && a.window > 0 ? max(max(x.pos0 + qi, 0) - a.window + 1, 0) : 0;
-        const int tmin = min(x.pos0 + (x.first + i * 128) / a.group + 1, x.len);
-        const int tmax = max(x.pos0 + (x.first + min(i * 128 + 128, x.rows) - 1) / a.group, 0);
+        {
+          // z: keys that all rows of the tile may see, w: the last row's position; in shared memory, as
+          // the registers are the scores'
+          const bool valid = r < x.rows;
+          const int p = x.pos0 + (x.first + r) / a.group;
+          sm.sight[r] = make_int4(valid ? min(p + 1, x.len) : x.len, valid && a.window > 0 ? max(max(p, 0) - a.window + 1, 0) : 0,
+                                  min(x.pos0 + (x.first + i * 128) / a.group + 1, x.len),
+                                  max(x.pos0 + (x.first + min(i * 128 + 128, x.rows) - 1) / a.group, 0));
+        }
         const uint64_t qs2 = f32x2(qsum, qsum);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          const int k0 = (t0 + j + (t0 + j >= sinks ? skip : 0)) * kKeys, st = (jt + j) & 3;
+          const int st = (jt + j) & 3;
           wait(&sm.par_full[st], ((jt + j) >> 2) & 1, &sm.dead, a.status);
           const float4 *kp = sm.kp[st];
           const uint2 hid = *reinterpret_cast<const uint2 *>(sm.hidden[st]);
-          const bool whole = (hid.x | hid.y) == 0 && k0 + kKeys <= tmin &&
-                             (a.window <= 0 || k0 > tmax - a.window || k0 + kKeys <= a.sinks);
+          const int k0 = (x.t0 + j + (x.t0 + j >= x.sinks ? x.skip : 0)) * kKeys;
+          const bool whole = (hid.x | hid.y) == 0 && k0 + kKeys <= sm.sight[r].z &&
+                             (a.window <= 0 || k0 > sm.sight[r].w - a.window || k0 + kKeys <= a.sinks);
           wait(&sm.s_full[i], (jn + j) & 1, &sm.dead, a.status);
           tc_fence_after();
           if (j + 1 == n) {  // the last scores are there, so the operand tile is free for the next rows
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
               // one bit per key, so that no lane branches
               const int kc = k0 + c * 32;
               const uint32_t off = (c < 2 ? hid.x : hid.y) >> ((c & 1) * 16);
-              const uint32_t seen = low_bits(vis - kc) & (~low_bits(wlo - kc) | low_bits(a.sinks - kc)) &
+              const uint32_t seen = low_bits(sm.sight[r].x - kc) & (~low_bits(sm.sight[r].y - kc) | low_bits(a.sinks - kc)) &
                                     ~((off & 1u) * 0xffffu | (off >> 8 & 1u) * 0xffff0000u);
 #pragma unroll
               for (int e = 0; e < 32; ++e) t.f[e] = seen & (1u << e) ? t.f[e] : -INFINITY;
@@ -561,14 +568,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         wait(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
         if (nx.n > 0) fetch_q(nx);
       }
-      jt += n;
+      jt += x.n;
       if (nx.n > 0) have_q(nx);
       // ---- the result.  Column c of O is dim 2c, column D/2 + c dim 2c + 1.
       if (active) {
         const float2 l0 = from_f32x2(la), l1 = from_f32x2(lb);
         const float sum = (l0.x + l0.y) + (l1.x + l1.y);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const bool valid = r < x.rows, begins = x.t0 == 0, full = begins && x.t0 + n == x.tiles;
+        const bool valid = r < x.rows, begins = x.t0 == 0, full = begins && x.t0 + x.n == x.tiles;
         const int rr = x.first + r, qi = rr / a.group;
         T *op = static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
                 (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head;
@@ -776,16 +783,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         __syncwarp();
       };
       // Per key tile and row tile: O += P V, then S of the next key tile, which may be the next item's.
-      int it = 0, j = 0, n = 0, row_tiles = 0;  // of the tile whose P V comes next
+      int it = 0, j = 0, n = 0, n0 = 0, row_tiles = 0;  // of the tile whose P V comes next
       uint32_t p_phase = 0, q_phase = 0;  // a bit per row tile
 #pragma unroll 1
       for (int jt = -1;; ++jt) {
-        int next_n = n, next_tiles = row_tiles;
+        int next_n = n, next_n0 = n0, next_tiles = row_tiles;
         const bool turn = j + 1 >= n;  // the next scores are another item's
         if (turn) {
           const int slot = (n ? it + 1 : it) % kItems;
           wait(&sm.item_full[slot], (n ? it + 1 : it) / kItems & 1, &sm.dead, a.status);
           next_n = sm.item[slot].n;
+          next_n0 = sm.item[slot].n0;
           next_tiles = next_n == 0 || sm.dead ? 0 : sm.item[slot].rows > 128 ? 2 : 1;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
@@ -793,14 +801,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         if (row_tiles) wait(&sm.v_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (i < row_tiles) {
+          if (i < row_tiles && (i || j < n0)) {
             wait(&sm.p_full[i], p_phase >> i & 1, &sm.dead, a.status);
             p_phase ^= 1u << i;
             tc_fence_after();
             pv(i, jt, j > 0);
           }
-          if (i < next_tiles) {
-            if (i == 0) wait(&sm.k_full[(jt + 1) & 1], ((jt + 1) / 2) & 1, &sm.dead, a.status);
+          if (i == 0 && next_tiles) wait(&sm.k_full[(jt + 1) & 1], ((jt + 1) / 2) & 1, &sm.dead, a.status);
+          if (i < next_tiles && (i || (turn ? 0 : j + 1) < next_n0)) {
             if (turn) {
               wait(&sm.q_full[i], q_phase >> i & 1, &sm.dead, a.status);
               q_phase ^= 1u << i;
@@ -821,6 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           ++j;
         }
         n = next_n;
+        n0 = next_n0;
         row_tiles = next_tiles;
       }
       if (elect_one()) mma_commit(&sm.done);  // nothing in flight when the CTA gives its memory back
@@ -831,14 +840,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       int it = 0, pj = 0;
       auto publish = [&](bool end) {
         if (it >= kItems) wait(&sm.item_empty[it % kItems], (it / kItems - 1) & 1, &sm.dead, a.status);
+        const int n = end ? 0 : w.t1 - w.t0, first = w.block * kRows;
+        const int seen0 = min(w.q.len, w.q.pos0 + (first + min(127, w.rows() - 1)) / a.group + 1);
+        const bool less = n > 1 && w.k.key0(w.t1 - 1) >= seen0;
         if (lane == 0)
-          sm.item[it % kItems] = Item{end ? 0 : w.t1 - w.t0, w.t0, w.k.tiles, w.k.sinks, w.k.skip, w.q.row0, w.rows(),
-                                      w.q.len, w.q.pos0, w.block * kRows, w.head};
+          sm.item[it % kItems] = Item{n, w.t0, w.k.tiles, w.k.sinks, w.k.skip, w.q.row0, w.rows(),
+                                      w.q.len, w.q.pos0, first, w.head, less ? n - 1 : n};
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.item_full[it % kItems]);
         ++it;
       };
-      Desc d{-1, 0, 0, 0};
+      Desc d{-1, 0, 0, 0, 0, {}};
       if (mylen > 0) {
         publish(false);
 #pragma unroll 1
@@ -877,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         }
         if (w.t0 == 0 && w.t1 < w.k.tiles) {
           const long long end = lo + mylen + (w.k.tiles - w.t1);
-          d = Desc{w.seq, w.block, w.head, static_cast<int>((end - 1) / quota)};
+          d = Desc{static_cast<int>((end - 1) / quota), w.q.row0, w.block * kRows, w.rows(), w.head, {}};
         }
       }
       publish(true);
@@ -891,43 +903,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   }
 }
 
-// Joins the parts of the item that starts in part blockIdx.x and ends later.
+// Joins the parts of the item that starts in part blockIdx.x and ends later: a warp a row, kJoin
+// rows a block.
+constexpr int kJoin = 32;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv4_tile_join_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(kJoin * 32) kv4_tile_join_kernel(const Kv4AttnArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const Desc x = reinterpret_cast<const Desc *>(a.work_tile)[blockIdx.x];
-  if (x.seq < 0) return;
+  const int r = blockIdx.y * kJoin + threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (x.last < 0 || r >= x.rows) return;
   const float *slots = a.work_tile + gridDim.x * (sizeof(Desc) / 4);
-  const Rows q = load_rows(a, x.seq);
-  const int c0 = blockIdx.x, rows = min(kRows, q.rows - x.block * kRows);
+  const int c0 = blockIdx.x;
   auto part = [&](int c) { return slots + (2 * static_cast<size_t>(c) + (c == c0)) * slot_floats(D); };
-  const int r = blockIdx.y * (1024 / D) + threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
-  if (r >= rows) return;
-  float mx = kNegBig, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // 32 parts at a time: a lane a part for the maximum and the factors, then all lanes for the sums
+  constexpr int V = D / 32;
+  float mx = kNegBig, sum = 0.f, acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int c = c0; c <= x.last; c += 32) {
+    const bool in = c + lane <= x.last;
+    const float m = in ? part(c + lane)[kRows * D + r] : kNegBig, l = in ? part(c + lane)[kRows * D + kRows + r] : 0.f;
+    float top = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, mx);
+    const float old = ex2f(mx - top), f = ex2f(m - top);
+    mx = top;
+    float fl = in ? f * l : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) fl += __shfl_xor_sync(0xffffffffu, fl, o);
+    sum = fmaf(sum, old, fl);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] *= old;
+    const int n = min(32, x.last - c + 1);
 #pragma unroll 4
-  for (int c = c0; c <= x.last; ++c) mx = fmaxf(mx, part(c)[kRows * D + r]);
-#pragma unroll 4
-  for (int c = c0; c <= x.last; ++c) {
-    const float *p = part(c);
-    const float f = ex2f(p[kRows * D + r] - mx);
-    const float4 v = *reinterpret_cast<const float4 *>(p + r * D + d);
-    sum = fmaf(f, p[kRows * D + kRows + r], sum);
-    acc.x = fmaf(f, v.x, acc.x);
-    acc.y = fmaf(f, v.y, acc.y);
-    acc.z = fmaf(f, v.z, acc.z);
-    acc.w = fmaf(f, v.w, acc.w);
+    for (int k = 0; k < n; ++k) {
+      const float w = __shfl_sync(0xffffffffu, f, k);
+      const float *p = part(c + k) + r * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+        acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+      }
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int rr = x.block * kRows + r, qi = rr / a.group;
-  T *op = static_cast<T *>(a.out) + (q.row0 + static_cast<int64_t>(qi)) * a.o_row +
-          (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head + d;
+  const int rr = x.first + r, qi = rr / a.group;
+  T *op = static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
+          (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head + lane * V;
   using X = Kv4Type<T>;
-  uint2 o;
-  o.x = kv4_bits<uint32_t>(X::from2(acc.x * inv, acc.y * inv));
-  o.y = kv4_bits<uint32_t>(X::from2(acc.z * inv, acc.w * inv));
-  *reinterpret_cast<uint2 *>(op) = o;
+#pragma unroll
+  for (int i = 0; i < V; i += 2)
+    *reinterpret_cast<uint32_t *>(op + i) = kv4_bits<uint32_t>(X::from2(acc[i] * inv, acc[i + 1] * inv));
 }
 
 template <typename T, int D>
@@ -949,8 +982,8 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.num_sms, kRows * D / 1024, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3(a.num_sms, kRows / kJoin, 1);
+  cfg.blockDim = dim3(kJoin * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv4_tile_join_kernel<T, D>, a);
 }
