@@ -407,9 +407,11 @@ mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_ro
  * over the visible keys; scores from K's codes and pairs as they are, scores, sums
  * and accumulation in fp32.  Sequences with at most 32 rows (new tokens times
  * grouped heads) per kv head take V's codes and pairs as they are too, weights
- * times V's scale in fp16 under a power of two; with more rows the weights and V's
- * rows are rounded to T for their product.  A row that sees no key is written as
- * zeros; a NaN in a row reaches only those queries that see the row.
+ * times V's scale in fp16 under a power of two (in two parts of fp16 for an fp16
+ * cache); with more rows the weights and V's rows are rounded to fp16 for their
+ * product (to bf16 for 16 tokens of a bf16 cache whose V values do not fit fp16).
+ * A row that sees no key is written as zeros; a NaN in a row reaches only those
+ * queries that see the row.
  *   q, out   [n_rows][n_q_heads][head_dim], strides in elements, multiples of 8;
  *            16-byte aligned; out must not overlap q
  *   max_new  a bound on cu[s+1] - cu[s], or 0 for none: it picks the kernel, the

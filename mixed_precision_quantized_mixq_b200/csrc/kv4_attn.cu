@@ -157,10 +157,9 @@ struct Place {  // of a part of an item
   int head, row0, row_first, rows;  // first q row of the sequence, first row and number of rows of the item
 };
 
-template <int D, int NT, int SLOTS>
+template <int D, int R, int SLOTS>
 struct Smem {
   static constexpr int REC = kv4_rec_bytes(D);
-  static constexpr int R = 8 * NT;
   static constexpr int OROW = D + 4;  // padded row: float2 stores of the four t lanes hit other banks
   alignas(128) uint8_t ring[kWarps][SLOTS][kUnit][REC];
   float m[2][kWarps][R], l[2][kWarps][R];  // [0]: the item that a warp's span begins in, [1]: the one it ends in
@@ -174,11 +173,14 @@ struct Smem {
   long long lo, quota;
 };
 
-template <typename T, int D, int NT, int SLOTS>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(const Kv4AttnArgs a) {
-  constexpr int R = 8 * NT, WORDS = D / 32, MT = D / 16, REC = kv4_rec_bytes(D);
+// R rows of an item: 16, 8, or 4 that take the 8 columns of a product twice.
+template <typename T, int D, int R, int SLOTS>
+__global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(const Kv4AttnArgs a) {
+  constexpr int NT = (R + 7) / 8, WORDS = D / 32, MT = D / 16, REC = kv4_rec_bytes(D);
   constexpr bool BF = Kv4Type<T>::bf16;
-  using S = Smem<D, NT, SLOTS>;
+  constexpr bool TWICE = R == 4;      // columns 4..7 are the second parts of rows 0..3
+  constexpr bool PARTS = !BF && R > 4;  // second parts have products of their own
+  using S = Smem<D, R, SLOTS>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   S &sm = *reinterpret_cast<S *>(smem_raw);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     float cs[NT][2], qs[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = row_first + nt * 8 + g;
+      const int r = row_first + (TWICE ? g & 3 : nt * 8 + g);
       const bool valid = r < rows_all;
       const int qi = r / a.group;
       const T *qp = static_cast<const T *>(a.q) + (cur.q.row0 + static_cast<int64_t>(qi)) * a.q_row +
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int rr = row_first + nt * 8 + 2 * t + j, p = cur.q.pos0 + rr / a.group;
+              const int rr = row_first + (TWICE ? 2 * (t & 1) : nt * 8 + 2 * t) + j, p = cur.q.pos0 + rr / a.group;
               const bool valid = rr < rows_all;
               vis[nt][j] = valid ? min(p + 1, cur.q.len) : 0x7fffffff;
               wlo[nt][j] = valid && a.window > 0 ? max(p, 0) - a.window + 1 : 0;
@@ -582,13 +584,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
           products(std::false_type{});
         else
           products(std::true_type{});
+        // For fp16 caches weights go in as two fp16 parts (22 bits): codes are all positive, so what a
+        // rounded weight is off by does not cancel against lo's part of the row, and an average over
+        // many keys was off by three times what its own rounding to fp16 is.  With four rows the
+        // columns 4..7 hold the second parts; else they are a product of their own (8 % of the kernel).
+        // A bf16 result is rounded eight times as far: one part is enough.
 #pragma unroll
         for (int r = 0; r < kUnit; ++r) {
-          uint32_t p0[NT], p1[NT];
+          uint32_t p0[NT], p1[NT], q0[NT], q1[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            p0[nt] = transpose8x8(pack_half2(p[r][nt][0], p[r][nt][1]));
-            p1[nt] = transpose8x8(pack_half2(p[r][nt][2], p[r][nt][3]));
+            const uint32_t h0 = pack_half2(p[r][nt][0], p[r][nt][1]), h1 = pack_half2(p[r][nt][2], p[r][nt][3]);
+            const float2 f0 = __half22float2(kv4_bits<__half2>(h0)), f1 = __half22float2(kv4_bits<__half2>(h1));
+            uint32_t d0 = 0, d1 = 0;
+            if (TWICE || PARTS) {
+              d0 = pack_half2(p[r][nt][0] - f0.x, p[r][nt][1] - f0.y);
+              d1 = pack_half2(p[r][nt][2] - f1.x, p[r][nt][3] - f1.y);
+            }
+            p0[nt] = transpose8x8(TWICE && t >= 2 ? d0 : h0);
+            p1[nt] = transpose8x8(TWICE && t >= 2 ? d1 : h1);
+            if (PARTS) {
+              q0[nt] = transpose8x8(d0);
+              q1[nt] = transpose8x8(d1);
+            }
           }
           const uint8_t *rec = sm.ring[warp][slot][r];
 #pragma unroll
@@ -597,11 +615,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             const uint32_t vw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t v8 = vw[i] >> 8;
+              const uint32_t v8 = vw[i] >> 8, a0 = vw[i] & 0x000f000fu, a1 = vw[i] & 0x00f000f0u, a2 = v8 & 0x000f000fu,
+                             a3 = v8 & 0x00f000f0u;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816(o[nt][4 * c + i], vw[i] & 0x000f000fu, vw[i] & 0x00f000f0u, v8 & 0x000f000fu,
-                         v8 & 0x00f000f0u, p0[nt], p1[nt]);
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816(o[nt][4 * c + i], a0, a1, a2, a3, p0[nt], p1[nt]);
+                if (PARTS) mma16816(o[nt][4 * c + i], a0, a1, a2, a3, q0[nt], q1[nt]);
+              }
             }
           }
         }
@@ -614,6 +634,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     // ---- the segment's result.  Rows 8 i + g of the products are dims 2 (8 i + g) (x 2^-24) and
     // 2 (8 i + g) + 1 (x 2^-20).
     const float un = 1.f / sig;
+    if (TWICE) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[0][i][j] += __shfl_xor_sync(0xffffffffu, o[0][i][j], 2);
+    }
     const bool begins = cur.start >= w0, ends = cur.start + cur.q.n_unit <= w1;
     // the second kind waits in the ring, which is empty by then; the first would be in its way
     const int which = begins ? 1 : 0;
@@ -635,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
           zj += __shfl_xor_sync(0xffffffffu, zj, x);
         }
         const int col = nt * 8 + 2 * t + j, rr = row_first + col;
-        if (rr >= rows_all) continue;
+        if (rr >= rows_all || (TWICE && t >= 2)) continue;
         if (begins && ends) {
           const float inv = lj == 0.f ? 0.f : 1.f / lj;
           const int qi = rr / a.group;
@@ -727,9 +753,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 }
 
 // Joins the parts of the item that starts in part blockIdx.x and ends later.
-template <typename T, int D, int NT>
+template <typename T, int D, int R>
 __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Kv4AttnArgs a) {
-  constexpr int R = 8 * NT;
   griddep_wait();
   griddep_launch_dependents();
   const Desc *desc = reinterpret_cast<const Desc *>(a.work);
@@ -771,16 +796,16 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Kv4AttnArgs a)
   }
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int R>
 cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
-  constexpr int SLOTS = D == 64 ? 5 : NT == 1 ? 3 : 5;  // units in flight: two CTAs fit an SM, or one with 16 rows
-  auto kernel = kv4_attn_kernel<T, D, NT, SLOTS>;
-  const int smem = static_cast<int>(sizeof(Smem<D, NT, SLOTS>));
+  constexpr int SLOTS = D == 64 ? 5 : R <= 8 ? 3 : 5;  // units in flight: two CTAs fit an SM, or one with 16 rows
+  auto kernel = kv4_attn_kernel<T, D, R, SLOTS>;
+  const int smem = static_cast<int>(sizeof(Smem<D, R, SLOTS>));
   static std::atomic<uint64_t> done{0};
   cudaError_t e = ensure_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.num_sms * (NT == 1 ? 2 : 1), 1, 1);
+  cfg.gridDim = dim3(a.num_sms * (R <= 8 ? 2 : 1), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -792,13 +817,16 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D, NT>, a);
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D, R>, a);
 }
 
 template <typename T, int D>
 cudaError_t pick(const Kv4AttnArgs &a, cudaStream_t stream) {
-  // 8 rows per tile while a sequence's rows of a kv head fit one such tile
-  return a.max_rows <= 8 ? launch<T, D, 1>(a, stream) : launch<T, D, 2>(a, stream);
+  // the fewest rows per item that take a sequence's rows of a kv head at once; four only where
+  // weights have second parts
+  if constexpr (!Kv4Type<T>::bf16)
+    if (a.max_rows <= 4) return launch<T, D, 4>(a, stream);
+  return a.max_rows <= 8 ? launch<T, D, 8>(a, stream) : launch<T, D, 16>(a, stream);
 }
 
 }  // namespace

@@ -7,7 +7,8 @@
 // the softmax of one runs, the tensor core works for the other.  Per key tile
 //   S = Q C^T   (C: K's codes, exact in the 16-bit type), 128 x 128 x D, in TMEM
 //   t = scale log2(e) (s_k S + lo_k sum(q)),  P = 2^(t - m)
-//   O += P V^   (V^: V's rows as they read back, rounded once to the type)
+//   O += P V^   (V^: V's rows as they read back, rounded once to fp16, or to bf16 where a
+//                bf16 cache's values do not fit fp16)
 // with P written over S in TMEM as the second product's A operand.
 //
 // Roles: warps 0-7 softmax (thread = query row = TMEM lane; no reduction crosses
@@ -15,7 +16,7 @@
 // swizzled operand tiles (one 16-token record a warp and tile, the next tile's
 // bytes already in registers), warp 16 issues the MMAs.  K stays in codes because
 // a rounded K would move every score; the pairs act on S instead.  V is rounded
-// to the type like any 16-bit V, which leaves the softmax no work per V row.
+// like any 16-bit V, which leaves the softmax no work per V row.
 //
 // The key tiles of all (sequence, 256 rows, head) items are one line, cut into
 // equal parts over a persistent grid of one CTA per SM: the load is even whatever
@@ -67,7 +68,7 @@ struct TileSmem {
   alignas(1024) uint8_t k[2][kKeys * D * 2];
   alignas(1024) uint8_t v[2][kKeys * D * 2];
   alignas(16) float4 kp[4][kKeys / 2];  // per pair of keys: s0 s1 lo0 lo1, times scale log2(e)
-  alignas(8) uint8_t hidden[4][8];  // records of the tile whose page is not usable
+  alignas(8) uint8_t hidden[4][8];  // of the tile's records: bit 0: the page is not usable, bit 1: bf16 products with V
   alignas(16) int4 sight[kRows];  // of a row: key j is seen when j < x and (j >= y or j < sinks); z, w: of its row tile
   Item item[kItems];
   int64_t src[2][32];  // records of four tiles: offset in the pages, -1 beyond the keys, -2 page not usable
@@ -131,6 +132,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// Whether a row of V with this pair leaves the range that fp16 holds to 11 bits (or nearly).
+__device__ __forceinline__ bool past_half(float2 v) {
+  const float top = fmaxf(fabsf(v.y), fabsf(fmaf(15.f, v.x, v.y)));
+  return !(top < 32768.f) || (top < 1.52587890625e-5f && top > 0.f);
 }
 
 template <typename T>
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           const float4 *kp = sm.kp[st];
           const uint2 hid = *reinterpret_cast<const uint2 *>(sm.hidden[st]);
           const int k0 = (x.t0 + j + (x.t0 + j >= x.sinks ? x.skip : 0)) * kKeys;
-          const bool whole = (hid.x | hid.y) == 0 && k0 + kKeys <= sm.sight[r].z &&
+          const bool whole = ((hid.x | hid.y) & 0x01010101u) == 0 && k0 + kKeys <= sm.sight[r].z &&
                              (a.window <= 0 || k0 > sm.sight[r].w - a.window || k0 + kKeys <= a.sinks);
           wait(&sm.s_full[i], (jn + j) & 1, &sm.dead, a.status);
           tc_fence_after();
@@ -520,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                  const float2 f = X::f2(kv4_bits<T2>(o[e]));
-                  o[e] = kv4_bits<uint32_t>(X::from2(f.x * al, f.y * al));
+                  const float2 f = __half22float2(kv4_bits<__half2>(o[e]));
+                  o[e] = kv4_bits<uint32_t>(__floats2half2_rn(f.x * al, f.y * al));
                 }
                 tmem_st16(tm_s(i) + lanes + x * 16, o);
               }
@@ -551,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
                 const float p0 = ex2f(x.x), p1 = ex2f(x.y);
                 if (e & 1) lb = add_f32x2(lb, f32x2(p0, p1));
                 else la = add_f32x2(la, f32x2(p0, p1));
-                p[e] = kv4_bits<uint32_t>(X::from2(p0, p1));
+                p[e] = kv4_bits<uint32_t>(__floats2half2_rn(p0, p1));
               }
               if (next) mx = scores(buf[h ^ 1], c + 1);
               tmem_st16(tm_s(i) + lanes + c * 16, p);
@@ -559,6 +566,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             }
           }
           tmem_st_wait();
+          if (BF && __builtin_expect((hid.x | hid.y) & 0x02020202u, 0)) {  // weights of bf16 products
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t w = (c < 2 ? hid.x : hid.y) >> ((c & 1) * 16);
+              uint32_t o[16];
+              tmem_ld16(tm_s(i) + lanes + c * 16, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (w >> (e / 8 * 8 + 1) & 1)
+                  o[e] = kv4_bits<uint32_t>(__float22bfloat162_rn(__half22float2(kv4_bits<__half2>(o[e]))));
+              tmem_st16(tm_s(i) + lanes + c * 16, o);
+            }
+            tmem_st_wait();
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.p_full[i]);
@@ -668,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           kp[0] = both ? own.x * sl2 : 0.f;
           kp[2] = both ? own.y * sl2 : NAN;
         }
-        if (lane == 0) sm.hidden[j & 3][rw] = gone;
+        const bool wide = BF && __any_sync(0xffffffffu, lane >= 16 && both && past_half(own));
+        if (lane == 0) sm.hidden[j & 3][rw] = (gone ? 1 : 0) | (wide ? 2 : 0);
         // ---- K codes: lane (g, t) has dims [t D/4, (t+1) D/4) of keys g and g + 8
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -710,39 +733,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         const bool both = finite(own);
         if (j >= 2) wait(&sm.v_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
         // transposed: tile row = dim (2b at b, 2b + 1 at D/2 + b), 64 keys per 128-byte atom
-        // (s, lo) of this lane's tokens 2t, 2t+1 and 2t+8, 2t+9 in the type
+        // (s, lo) of this lane's tokens 2t, 2t+1 and 2t+8, 2t+9
         const uint32_t use = both ? pr : 0u;
         uint32_t q[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) q[e] = __shfl_sync(0xffffffffu, use, 16 + 2 * t + (e & 1) + 8 * (e >> 1));
-        const T2 s0 = kv4_bits<T2>(__byte_perm(q[0], q[1], 0x5410)), l0 = kv4_bits<T2>(__byte_perm(q[0], q[1], 0x7632));
-        const T2 s1 = kv4_bits<T2>(__byte_perm(q[2], q[3], 0x5410)), l1 = kv4_bits<T2>(__byte_perm(q[2], q[3], 0x7632));
-        const T2 top = X::from2(X::max_finite, X::max_finite);
         const int c0 = (rw & 3) * 2;  // chunk of tokens 0..7 of the record
         uint8_t *v0 = sm.v[st] + (rw / 4) * (D * 128) + g * 128 + 4 * t + ((c0 ^ g) << 4);
         uint8_t *v1 = sm.v[st] + (rw / 4) * (D * 128) + g * 128 + 4 * t + (((c0 + 1) ^ g) << 4);
-        auto rows = [&](auto clamp) {
-#pragma unroll
+        // o = (dim 2b, tokens 2t..), (2b + 1, 2t..), (2b, 2t+8..), (2b + 1, 2t+8..)
+        auto rows = [&](auto type, auto rare, const auto (&sc)[2], const auto (&of)[2]) {
+          using U = decltype(type);
+          using U2 = typename Kv4Type<U>::T2;
+          const U2 top = Kv4Type<U>::from2(Kv4Type<U>::max_finite, Kv4Type<U>::max_finite);
+#pragma unroll(rare.value ? 1 : D / 64)
           for (int c = 0; c < D / 64; ++c) {
-            const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+            const uint4 xc = rare.value && c ? x[D / 64 - 1] : x[rare.value ? 0 : c];
+            const uint32_t y[4] = {xc.x, xc.y, xc.z, xc.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              T2 o[4];  // (dim 2b, tokens 2t..), (2b + 1, 2t..), (2b, 2t+8..), (2b + 1, 2t+8..)
-              Codes<T>::pairs(y[e], o);
+              U2 o[4];
+              Codes<U>::pairs(y[e], o);
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
-                o[z] = __hfma2(o[z], z < 2 ? s0 : s1, z < 2 ? l0 : l1);
-                if (clamp.value) o[z] = __hmin2(o[z], top);
-                *reinterpret_cast<T2 *>((z < 2 ? v0 : v1) + (c * 32 + e * 8) * 128 + (z & 1) * D * 64) = o[z];
+                o[z] = __hfma2(o[z], sc[z / 2], of[z / 2]);
+                if (rare.value) o[z] = __hmin2(o[z], top);
+                *reinterpret_cast<U2 *>((z < 2 ? v0 : v1) + (c * 32 + e * 8) * 128 + (z & 1) * D * 64) = o[z];
               }
             }
           }
         };
-        // 15 s + lo can pass the type's largest value (s is rounded): hold it there
-        if (__builtin_expect(__any_sync(0xffffffffu, fmaf(15.f, own.x, own.y) > X::max_finite), 0))
-          rows(std::true_type{});
-        else
-          rows(std::false_type{});
+        // bf16 rows go in as fp16, which holds them eight times as exactly, while they are in its
+        // range.  15 s + lo can pass the type's largest value (s is rounded): hold it there.
+        const bool wide = BF && __any_sync(0xffffffffu, lane >= 16 && both && past_half(own));
+        if (BF && __builtin_expect(!wide, 1)) {
+          __half2 sc[2], of[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 u = kv4_pair<BF>(q[2 * h]), w = kv4_pair<BF>(q[2 * h + 1]);
+            sc[h] = __floats2half2_rn(u.x, w.x);
+            of[h] = __floats2half2_rn(u.y, w.y);
+          }
+          rows(__half{}, std::false_type{}, sc, of);
+        } else {
+          T2 sc[2], of[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sc[h] = kv4_bits<T2>(__byte_perm(q[2 * h], q[2 * h + 1], 0x5410));
+            of[h] = kv4_bits<T2>(__byte_perm(q[2 * h], q[2 * h + 1], 0x7632));
+          }
+          if (BF || __builtin_expect(__any_sync(0xffffffffu, fmaf(15.f, own.x, own.y) > X::max_finite), 0))
+            rows(T{}, std::true_type{}, sc, of);
+          else
+            rows(T{}, std::false_type{}, sc, of);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.v_full[st]);
@@ -754,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     if (warp == 24) {
       // --------------------------------------------------------------- MMA
       constexpr uint32_t kind = BF ? (1u << 7) | (1u << 10) : 0u;
-      constexpr uint32_t id_qk = idesc_f16_f32(128, kKeys) | kind, id_pv = idesc_f16_f32(128, D) | kind;
+      constexpr uint32_t id_qk = idesc_f16_f32(128, kKeys) | kind, id_pv = idesc_f16_f32(128, D);
       const uint64_t q_desc = sw128_kmajor_desc(smem_u32(sm.q)), k_desc = sw128_kmajor_desc(smem_u32(sm.k)),
                      v_desc = sw128_kmajor_desc(smem_u32(sm.v));
       constexpr uint32_t kStage = 128 * D * 2 >> 4;  // an operand tile, in the descriptors' units
@@ -772,11 +816,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       };
       auto pv = [&](int i, int jt, bool add) {
         const uint64_t vd = v_desc + (jt & 1) * kStage;
+        // a byte per record, that is per 16 keys
+        const uint64_t wide = BF ? *reinterpret_cast<const uint64_t *>(sm.hidden[jt & 3]) & 0x0202020202020202ull : 0;
         if (elect_one()) {
+          if (BF && __builtin_expect(wide != 0, 0)) {
+#pragma unroll 1
+            for (int x = 0; x < kKeys / 16; ++x)
+              mma_f16_ts(tm_o(i), tm_s(i) + x * 8, vd + (x / 4) * ((D * 128) >> 4) + (x % 4) * 2,
+                         wide >> (8 * x) & 2 ? id_pv | kind : id_pv, add || x > 0);
+          } else {
 #pragma unroll
-          for (int x = 0; x < kKeys / 16; ++x) {
-            const uint64_t adv = (x / 4) * ((D * 128) >> 4) + (x % 4) * 2;
-            mma_f16_ts(tm_o(i), tm_s(i) + x * 8, vd + adv, id_pv, add || x > 0);
+            for (int x = 0; x < kKeys / 16; ++x)
+              mma_f16_ts(tm_o(i), tm_s(i) + x * 8, vd + (x / 4) * ((D * 128) >> 4) + (x % 4) * 2, id_pv, add || x > 0);
           }
           mma_commit(&sm.o_full[i]);
         }

@@ -120,7 +120,9 @@ def attention(pages: Pages, q, table, lens, cu, scale, window=0, sinks=0):
         B = sum p |lo| / sum p;
       where a sequence has more than 32 rows per kv head, the tile kernel's operands: weights and V
         rows rounded once each to the type, so every term p v is off by at most 2 (eps/2) |p v|:
-        eps C with C = sum p |v| / sum p (second-order terms are below the fp32 allowance above)."""
+        eps C with C = sum p |v| / sum p (second-order terms are below the fp32 allowance above);
+        for a bf16 cache the type of that product is fp16, or bf16 for records that do not fit it, whose
+        weights are rounded to fp16 first: 2^-12 C more."""
     D = pages.D
     rows, heads = q.shape[0], q.shape[1]
     n_kv = pages.p.shape[1]
@@ -159,7 +161,8 @@ def attention(pages: Pages, q, table, lens, cu, scale, window=0, sinks=0):
                     + (2 * delta + 2.0 ** -17 * (1 + m / 2048)) * (A.abs() + B)
                     + torch.finfo(pages.dtype).smallest_normal * eps)
                 if (r1 - r0) * group > 32:
-                    tol[i, h * group:(h + 1) * group] += 2 * eps * (w @ vv.abs())
+                    step = 2 * eps + (2.0 ** -12 if pages.dtype == torch.bfloat16 else 0.0)
+                    tol[i, h * group:(h + 1) * group] += step * (w @ vv.abs())
     return out, tol
 
 

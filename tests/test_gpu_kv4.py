@@ -433,6 +433,36 @@ def test_value_scales_far_apart(factor, new):
     attend(21, [300, 140], new, 8, 2, D, page, F16, prepare=prepare)
 
 
+@pytest.mark.parametrize("new", [None, [3, 140, 260]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bf16_values_out_of_fp16_range(new, D):
+    """V rows far above fp16's largest value and far below its smallest, whole records of them and single tokens,
+    under scores that rise so that weights of both kinds are scaled again."""
+    page = 32
+
+    def prepare(host, table, q):
+        p = host.p.view(host.p.shape[0], 2, -1, 16 * (D + 8))
+        pairs = p[..., 16 * D:].contiguous().view(BF16).view(*p.shape[:3], 2, 16, 2)
+        for b in range(table.shape[0]):
+            for slot in range(int((table[b] >= 0).sum())):
+                v = pairs[int(table[b, slot]), :, :, 1]
+                kind = slot % 5
+                if kind == 1:
+                    v *= 2.0 ** 20
+                elif kind == 2:
+                    v *= 2.0 ** -30
+                elif kind == 3:
+                    v[:, 0, 7] *= 2.0 ** 18  # one token of the page's first record
+                elif kind == 4:
+                    v[:, 1, ::2] = 0.0
+                if b == 1:
+                    pairs[int(table[b, slot]), :, :, 0, :, 1] += 0.6 * slot  # K's lo
+        p[..., 16 * D:] = pairs.flatten(-3).view(torch.uint8)
+        q.abs_()
+
+    attend(27, [300, 400, 260], new, 8, 2, D, page, BF16, prepare=prepare)
+
+
 @pytest.mark.parametrize("new", [None, [2, 200]])
 def test_rising_scores(new):
     """Scores that grow along the sequence move the running maximum in almost every record."""
