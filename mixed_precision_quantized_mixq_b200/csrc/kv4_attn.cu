@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
     // negative position sees nothing: 0 stands for it, and no difference leaves 32 bits)
     const int edge_min = max(pmin, 0) - a.window, edge_max = max(pmax, 0) - a.window;
 
-    float o[NT][MT][4], m[NT][2], l[NT][2], z[NT][2];
+    float o[NT][MT][4], e[NT][4], m[NT][2], l[NT][2], z[NT][2];  // e: 7 times the weights' sums, as o sums them
     float lim[NT][2];  // a sum of weights above this moves the maximum m (0 before the first key)
     float sig = pow2(100);
 #pragma unroll
@@ -390,6 +390,8 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[nt][j] = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         m[nt][j] = 0.f;
@@ -549,6 +551,8 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
               al[j] *= f;
             }
 #pragma unroll
+            for (int j = 0; j < 4; ++j) e[nt][j] *= al[j & 1];
+#pragma unroll
             for (int i = 0; i < MT; ++i) {
               o[nt][i][0] *= al[0];
               o[nt][i][1] *= al[1];
@@ -565,6 +569,10 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
 #pragma unroll
           for (int r = 0; r < kUnit; ++r) {
             const float s0 = vs[r][0] * sig, s1 = vs[r][1] * sig;
+            if (!BF) {
+              vl[r][0] = fmaf(7.f, vs[r][0], vl[r][0]);
+              vl[r][1] = fmaf(7.f, vs[r][1], vl[r][1]);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -584,11 +592,14 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
           products(std::false_type{});
         else
           products(std::true_type{});
-        // For fp16 caches weights go in as two fp16 parts (22 bits): codes are all positive, so what a
-        // rounded weight is off by does not cancel against lo's part of the row, and an average over
-        // many keys was off by three times what its own rounding to fp16 is.  With four rows the
-        // columns 4..7 hold the second parts; else they are a product of their own (8 % of the kernel).
-        // A bf16 result is rounded eight times as far: one part is enough.
+        // Codes are all positive, so what the products lose does not cancel against lo's part of the
+        // row, and the mean over a long context is small beside both.  A bf16 result is rounded far
+        // enough to hide that.  For fp16 caches
+        //   weights go in as two fp16 parts (22 bits); with four rows the columns 4..7 hold the second
+        //   parts, else they are a product of their own (8 % of the kernel);
+        //   a row of sevens among the codes sums what the same instructions make of the weights, which
+        //   takes out, with 7 s beside lo, what their sums lose by being cut off (131072 tokens: 8e-4
+        //   of the result otherwise).
 #pragma unroll
         for (int r = 0; r < kUnit; ++r) {
           uint32_t p0[NT], p1[NT], q0[NT], q1[NT];
@@ -606,6 +617,13 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
             if (PARTS) {
               q0[nt] = transpose8x8(d0);
               q1[nt] = transpose8x8(d1);
+            }
+          }
+          if (!BF) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(e[nt], 0x00070007u, 0x00700070u, 0x00070007u, 0x00700070u, p0[nt], p1[nt]);
+              if (PARTS) mma16816(e[nt], 0x00070007u, 0x00700070u, 0x00070007u, 0x00700070u, q0[nt], q1[nt]);
             }
           }
           const uint8_t *rec = sm.ring[warp][slot][r];
@@ -639,6 +657,16 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[0][i][j] += __shfl_xor_sync(0xffffffffu, o[0][i][j], 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[0][j] += __shfl_xor_sync(0xffffffffu, e[0][j], 2);
+    }
+    if (!BF) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nt][i][j] -= e[nt][j];
     }
     const bool begins = cur.start >= w0, ends = cur.start + cur.q.n_unit <= w1;
     // the second kind waits in the ring, which is empty by then; the first would be in its way
