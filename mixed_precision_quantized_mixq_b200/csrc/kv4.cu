@@ -16,7 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "kv4.h"
-#include "ptx.cuh"
+#include "kv4_ptx.cuh"
 
 namespace mixq {
 namespace {

@@ -31,7 +31,7 @@
 #include <type_traits>
 
 #include "kv4.h"
-#include "ptx.cuh"
+#include "kv4_ptx.cuh"
 #include "tma_host.h"
 
 namespace mixq {
