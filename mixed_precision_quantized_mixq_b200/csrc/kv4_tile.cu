@@ -114,10 +114,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Whether a row of V with this pair leaves the range that fp16 holds to 11 bits (or nearly).
+// Whether fp16 would hold a row of V with this bf16 pair worse than bf16: it reaches 2^15, or s or
+// lo is not exact in fp16, or s is so small that fp16's smallest step (2^-24) shows beside it.
 __device__ __forceinline__ bool past_half(float2 v) {
-  const float top = fmaxf(fabsf(v.y), fabsf(fmaf(15.f, v.x, v.y)));
-  return !(top < 32768.f) || (top < 1.52587890625e-5f && top > 0.f);
+  const float s = fabsf(v.x), lo = fabsf(v.y), top = fmaxf(lo, fabsf(fmaf(15.f, v.x, v.y)));
+  return !(top < 32768.f) || (s < 1.220703125e-4f && s > 0.f) || (lo < 7.62939453125e-6f && lo > 0.f);
 }
 
 template <typename T>

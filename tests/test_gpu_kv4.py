@@ -433,6 +433,24 @@ def test_value_scales_far_apart(factor, new):
     attend(21, [300, 140], new, 8, 2, D, page, F16, prepare=prepare)
 
 
+@pytest.mark.parametrize("power", [-7, -10, -12, -14, -17, -20, 10, 13, 16])
+def test_bf16_values_at_the_ends_of_fp16_range(power):
+    """Single keys (outputs are V rows) whose scales and smallest values lie about the ends of fp16's range."""
+    D, page = 64, 16
+
+    def prepare(host, table, q):
+        p = host.p.view(host.p.shape[0], 1, -1, 16 * (D + 8))
+        pairs = p[..., 16 * D:].contiguous().view(BF16).view(*p.shape[:3], 2, 16, 2)
+        pairs[..., 1, :, :] *= 2.0 ** power
+        pairs[..., 1, ::2, 1] *= 2.0 ** -6
+        pairs[..., 1, ::5, 0] = 0.0
+        pairs[..., 1, ::3, 1] = 0.0
+        p[..., 16 * D:] = pairs.flatten(-3).view(torch.uint8)
+
+    attend(28, [90, 45], [90, 45], 2, 1, D, page, BF16, prepare=prepare, window=1)
+    attend(29, [90, 45], [90, 45], 2, 1, D, page, BF16, prepare=prepare)
+
+
 @pytest.mark.parametrize("new", [None, [3, 140, 260]])
 @pytest.mark.parametrize("D", [64, 128])
 def test_bf16_values_out_of_fp16_range(new, D):
