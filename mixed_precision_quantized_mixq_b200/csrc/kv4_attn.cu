@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "kv4.h"
+#include "kv4_join.cuh"
 #include "kv4_ptx.cuh"
 #include "tma_host.h"
 
@@ -45,10 +46,6 @@ constexpr int kUnit = 2;       // records
 constexpr int kUnitKeys = kUnit * kKv4Rec;
 constexpr int kMinQuota = 8;   // units: below one a warp, a cut costs more than it spreads
 constexpr int kMaxRows = 16;
-
-struct Desc {  // item whose last part is not in the CTA that starts it
-  int seq, item, last, pad;
-};
 
 __host__ __device__ constexpr size_t slot_floats(int d) { return kMaxRows * static_cast<size_t>(d) + 2 * kMaxRows; }
 
@@ -112,12 +109,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return kv4_bits<uint32_t>(__floats2half2_rn(a, b));
 }
@@ -153,7 +144,7 @@ struct Walk {
 };
 
 struct Place {  // of a part of an item
-  int seq, item, end;  // where the item ends in the CTA's part of the line
+  int end;  // where the item ends in the CTA's part of the line
   int head, row0, row_first, rows;  // first q row of the sequence, first row and number of rows of the item
 };
 
@@ -163,7 +154,8 @@ struct Smem {
   static constexpr int OROW = D + 4;  // padded row: float2 stores of the four t lanes hit other banks
   alignas(128) uint8_t ring[kWarps][SLOTS][kUnit][REC];
   float m[2][kWarps][R], l[2][kWarps][R];  // [0]: the item that a warp's span begins in, [1]: the one it ends in
-  int part[kWarps];                        // bit 0: the first is there, 1: and ends here, 2: the second is there, 3: no span
+  // bit 0: the first is there, 1: and ends here, 4: and is in the ring; 2: the second is there; 3: no span
+  int part[kWarps];
   Place place[2][kWarps];
   uint64_t full[kWarps][SLOTS];
   int ok[kWarps][SLOTS];  // a bit per record
@@ -216,12 +208,12 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
   const long long quota = per > kMinQuota ? per : kMinQuota;
   const long long lo = min(static_cast<long long>(blockIdx.x) * quota, total);
   const int mylen = static_cast<int>(min(quota, total - lo));
-  Desc *desc = reinterpret_cast<Desc *>(a.work);
-  auto slots = [&]() { return a.work + gridDim.x * (sizeof(Desc) / 4); };
+  Kv4Join *desc = reinterpret_cast<Kv4Join *>(a.work);
+  auto slots = [&]() { return a.work + gridDim.x * (sizeof(Kv4Join) / 4); };
   auto heads = [&]() { return slots() + 2 * gridDim.x * slot_floats(D) + static_cast<size_t>(blockIdx.x) * kWarps * R * D; };
   if (tid == 0) sm.lo = lo, sm.quota = quota;  // kept there, not in registers
   if (mylen == 0) {
-    if (tid == 0) desc[blockIdx.x].seq = -1;
+    if (tid == 0) desc[blockIdx.x].last = -1;
     return;
   }
   // the sequence that holds position lo
@@ -506,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
               for (int r = 0; r < kUnit; ++r) {
-                p[r][nt][j] = ex2(s[r][nt][j]);
-                p[r][nt][j + 2] = ex2(s[r][nt][j + 2]);
+                p[r][nt][j] = ex2f(s[r][nt][j]);
+                p[r][nt][j + 2] = ex2f(s[r][nt][j + 2]);
               }
               sum[nt][j] = (p[0][nt][j] + p[0][nt][j + 2]) + (p[1][nt][j] + p[1][nt][j + 2]);
               over |= sum[nt][j] > lim[nt][j];
@@ -538,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
               n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16));
               const bool seen = lim[nt][j] > 0.f;
               const float d = n > (seen ? 0.f : -INFINITY) ? n : 0.f;
-              al[j] = seen ? ex2(-d) : 1.f;  // nothing to scale before the first key
+              al[j] = seen ? ex2f(-d) : 1.f;  // nothing to scale before the first key
               if (n > -INFINITY) lim[nt][j] = 256.f;
               m[nt][j] += d;
 #pragma unroll
@@ -669,14 +661,15 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
           for (int j = 0; j < 4; ++j) o[nt][i][j] -= e[nt][j];
     }
     const bool begins = cur.start >= w0, ends = cur.start + cur.q.n_unit <= w1;
-    // the second kind waits in the ring, which is empty by then; the first would be in its way
+    // a part that ends the span waits in the ring, which is empty by then
     const int which = begins ? 1 : 0;
-    float *part = begins ? reinterpret_cast<float *>(sm.ring[warp]) : heads() + warp * (R * D);
-    const int pitch = begins ? S::OROW : D;
-    if (!begins) parts |= ends ? 3 : 1;
+    const bool at_end = seg_end == w1;
+    float *part = at_end ? reinterpret_cast<float *>(sm.ring[warp]) : heads() + warp * (R * D);
+    const int pitch = at_end ? S::OROW : D;
+    if (!begins) parts |= (ends ? 3 : 1) | (at_end ? 16 : 0);
     if (begins && !ends) parts |= 4;
     if (lane == 0 && !(begins && ends))
-      sm.place[which][warp] = Place{cur.seq, cur.item, cur.start + cur.q.n_unit, head, cur.q.row0, row_first,
+      sm.place[which][warp] = Place{cur.start + cur.q.n_unit, head, cur.q.row0, row_first,
                                     min(R, rows_all - row_first)};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -716,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
 
   // ---- join the warps, a warp an item: those that begin in warp b's span, or in the CTA before
   // (b == -1), and go on
-  if (tid == 0) desc[blockIdx.x].seq = -1;
+  if (tid == 0) desc[blockIdx.x].last = -1;
   __syncthreads();
 #pragma unroll 1
   for (int b = warp - 1; b < kWarps; b += kWarps) {
@@ -733,8 +726,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
     const Place x = b < 0 ? sm.place[0][0] : sm.place[1][b];
     const bool full = b >= 0 && ends;
     if (b >= 0 && !ends && lane == 0)
-      desc[blockIdx.x] = Desc{x.seq, x.item, static_cast<int>((sm.lo + x.end - 1) / sm.quota), 0};
-    const float *tail = b < 0 ? nullptr : reinterpret_cast<const float *>(sm.ring[b]);
+      desc[blockIdx.x] = Kv4Join{static_cast<int>((sm.lo + x.end - 1) / sm.quota), x.row0, x.row_first, x.rows, x.head, {}};
     float *part = slots() + (2 * static_cast<size_t>(blockIdx.x) + (b < 0 ? 0 : 1)) * slot_floats(D);
 #pragma unroll 1
     for (int e = lane; e < x.rows * (D / 4); e += 32) {
@@ -744,17 +736,20 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
         if (sm.part[w] & 1) mx = fmaxf(mx, sm.m[0][w][r]);
       float sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](const float4 &o, float mw, float lw) {
-        const float f = ex2(mw - mx);
-        sum = fmaf(f, lw, sum);
+#pragma unroll 1
+      for (int w = max(b, 0); w <= last; ++w) {
+        const bool second = w == b;
+        if (!second && !(sm.part[w] & 1)) continue;
+        const float *p = second || sm.part[w] & 16 ? reinterpret_cast<const float *>(sm.ring[w]) + r * S::OROW
+                                                   : heads() + w * (R * D) + r * D;
+        const float4 o = *reinterpret_cast<const float4 *>(p + d);
+        const float f = ex2f(sm.m[second][w][r] - mx);
+        sum = fmaf(f, sm.l[second][w][r], sum);
         acc.x = fmaf(f, o.x, acc.x);
         acc.y = fmaf(f, o.y, acc.y);
         acc.z = fmaf(f, o.z, acc.z);
         acc.w = fmaf(f, o.w, acc.w);
-      };
-      if (b >= 0) add(*reinterpret_cast<const float4 *>(tail + r * S::OROW + d), sm.m[1][b][r], sm.l[1][b][r]);
-      for (int w = b + 1; w <= last; ++w)
-        if (sm.part[w] & 1) add(*reinterpret_cast<const float4 *>(heads() + w * (R * D) + r * D + d), sm.m[0][w][r], sm.l[0][w][r]);
+      }
       if (full) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int rr = x.row_first + r, qi = rr / a.group;
@@ -780,48 +775,20 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
       mbar_wait(&sm.full[warp][n % SLOTS], n / SLOTS & 1, kWaitNs / 16);
 }
 
-// Joins the parts of the item that starts in part blockIdx.x and ends later.
+// Joins the parts of the item that starts in part blockIdx.x and ends later, a warp a row.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(R * 32) kv4_join_kernel(const Kv4AttnArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const Desc *desc = reinterpret_cast<const Desc *>(a.work);
-  const float *slots = a.work + gridDim.x * (sizeof(Desc) / 4);
-  const Desc x = desc[blockIdx.x];
-  if (x.seq < 0) return;
-  const Seq q = load_seq<R>(a, x.seq);
-  const int head = x.item / q.tiles, row_first = (x.item - head * q.tiles) * R;
-  const int rows_all = q.nq * a.group, c0 = blockIdx.x;
-  for (int e = threadIdx.x; e < R * D / 4; e += kThreads) {
-    const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-    const int rr = row_first + r;
-    if (rr >= rows_all) continue;
-    float mx = kNegBig, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = c0; c <= x.last; ++c)
-      mx = fmaxf(mx, slots[(2 * c + (c == c0)) * slot_floats(D) + kMaxRows * D + r]);
-#pragma unroll 4
-    for (int c = c0; c <= x.last; ++c) {
-      const float *p = slots + (2 * c + (c == c0)) * slot_floats(D);
-      const float f = ex2(p[kMaxRows * D + r] - mx);
-      const float4 v = *reinterpret_cast<const float4 *>(p + r * D + d);
-      sum = fmaf(f, p[kMaxRows * D + kMaxRows + r], sum);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int qi = rr / a.group;
-    T *op = static_cast<T *>(a.out) + (q.row0 + static_cast<int64_t>(qi)) * a.o_row +
-            (static_cast<int64_t>(head) * a.group + (rr - qi * a.group)) * a.o_head + d;
-    using X = Kv4Type<T>;
-    uint2 o;
-    o.x = kv4_bits<uint32_t>(X::from2(acc.x * inv, acc.y * inv));
-    o.y = kv4_bits<uint32_t>(X::from2(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2 *>(op) = o;
-  }
+  const Kv4Join x = reinterpret_cast<const Kv4Join *>(a.work)[blockIdx.x];
+  const int r = threadIdx.x / 32, c0 = blockIdx.x;
+  if (x.last < 0 || r >= x.rows) return;
+  const float *slots = a.work + gridDim.x * (sizeof(Kv4Join) / 4);
+  auto part = [&](int c) { return slots + (2 * static_cast<size_t>(c) + (c == c0)) * slot_floats(D); };
+  const int rr = x.first + r, qi = rr / a.group;
+  kv4_join_row<D>(part, c0, x.last, kMaxRows, r, threadIdx.x & 31,
+                  static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
+                      (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head);
 }
 
 template <typename T, int D, int R>
@@ -844,6 +811,7 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
+  cfg.blockDim = dim3(R * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D, R>, a);
 }
@@ -863,7 +831,7 @@ size_t kv4_step_workspace(int d, int num_sms) {
   const size_t ctas = 2 * static_cast<size_t>(num_sms);
   // an item's first and last part of each CTA, and 8 rows that each warp leaves for its CTA (or half
   // the CTAs with 16)
-  return ctas * sizeof(Desc) + ctas * 2 * slot_floats(d) * sizeof(float) + ctas * kWarps * 8 * d * sizeof(float);
+  return ctas * sizeof(Kv4Join) + ctas * 2 * slot_floats(d) * sizeof(float) + ctas * kWarps * 8 * d * sizeof(float);
 }
 
 cudaError_t launch_kv4_attn(Kv4AttnArgs a, cudaStream_t stream) {

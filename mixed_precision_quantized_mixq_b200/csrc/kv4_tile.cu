@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include "kv4.h"
+#include "kv4_join.cuh"
 #include "kv4_ptx.cuh"
 #include "tma_host.h"
 
@@ -80,12 +81,6 @@ struct TileSmem {
   uint32_t tmem;
   int dead;
 };
-
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Bounded wait; once one has run out, none waits any more and the CTA winds up.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile int *dead, int32_t *status) {
@@ -229,11 +224,7 @@ struct Walk {
   __device__ __forceinline__ int rows() const { return min(kRows, q.rows - block * kRows); }
 };
 
-struct Desc {  // item whose last part is not in the CTA that starts it
-  int last;               // CTA of the last part, -1: no such item
-  int row0, first, rows;  // as in Item
-  int head, pad[3];
-};
+using Desc = Kv4Join;
 
 __host__ __device__ constexpr size_t slot_floats(int d) { return kRows * (static_cast<size_t>(d) + 2); }
 
@@ -949,50 +940,10 @@ __global__ void __launch_bounds__(kJoin * 32) kv4_tile_join_kernel(const Kv4Attn
   const float *slots = a.work_tile + gridDim.x * (sizeof(Desc) / 4);
   const int c0 = blockIdx.x;
   auto part = [&](int c) { return slots + (2 * static_cast<size_t>(c) + (c == c0)) * slot_floats(D); };
-  // 32 parts at a time: a lane a part for the maximum and the factors, then all lanes for the sums
-  constexpr int V = D / 32;
-  float mx = kNegBig, sum = 0.f, acc[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 1
-  for (int c = c0; c <= x.last; c += 32) {
-    const bool in = c + lane <= x.last;
-    const float m = in ? part(c + lane)[kRows * D + r] : kNegBig, l = in ? part(c + lane)[kRows * D + kRows + r] : 0.f;
-    float top = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    top = fmaxf(top, mx);
-    const float old = ex2f(mx - top), f = ex2f(m - top);
-    mx = top;
-    float fl = in ? f * l : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) fl += __shfl_xor_sync(0xffffffffu, fl, o);
-    sum = fmaf(sum, old, fl);
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] *= old;
-    const int n = min(32, x.last - c + 1);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float w = __shfl_sync(0xffffffffu, f, k);
-      const float *p = part(c + k) + r * D + lane * V;
-      if constexpr (V == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(p);
-        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
-      }
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int rr = x.first + r, qi = rr / a.group;
-  T *op = static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
-          (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head + lane * V;
-  using X = Kv4Type<T>;
-#pragma unroll
-  for (int i = 0; i < V; i += 2)
-    *reinterpret_cast<uint32_t *>(op + i) = kv4_bits<uint32_t>(X::from2(acc[i] * inv, acc[i + 1] * inv));
+  kv4_join_row<D>(part, c0, x.last, kRows, r, lane,
+                  static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
+                      (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head);
 }
 
 template <typename T, int D>
