@@ -12,22 +12,35 @@
 // with P written over S in TMEM as the second product's A operand.
 //
 // Roles: warps 0-7 softmax (thread = query row = TMEM lane; no reduction crosses
-// lanes), warps 8-15 unpack the cache straight from global memory into the
-// swizzled operand tiles (one 16-token record a warp and tile, the next tile's
-// bytes already in registers), warp 16 issues the MMAs.  K stays in codes because
-// a rounded K would move every score; the pairs act on S instead.  V is rounded
-// like any 16-bit V, which leaves the softmax no work per V row.
+// lanes); warps 8-15 unpack K's codes and warps 16-23 V's rows straight from global
+// memory into the swizzled operand tiles, one 16-token record a warp and tile, the
+// next tile's bytes already in registers; warp 24 issues the MMAs; warp 25 walks the
+// work ahead of them and hands out items and the places of records.  K stays in codes
+// because a rounded K would move every score; the pairs act on S instead.  V is
+// rounded like any 16-bit V, which leaves the softmax no work per V row.
 //
-// The key tiles of all (sequence, 256 rows, head) items are one line, cut into
-// equal parts over a persistent grid of one CTA per SM: the load is even whatever
-// the lengths and however few items there are, and the roles run on from item to
-// item, so one item's last softmax and output overlap the next one's first tiles.
-// An item cut by a boundary leaves fp32 partial results, joined by a second launch
-// in the order of the parts.
+// The key tiles of all (sequence, 256 rows, head) items are one line, cut into equal
+// parts over a persistent grid of one CTA per SM: the load is even whatever the
+// lengths and however few items there are.  The roles run on from item to item: the
+// next item's query rows are fetched during the last tile of this one, and its first
+// scores are computed beside this one's last product.  An item cut by a boundary
+// leaves fp32 partial results, joined by a second launch in the order of the parts.
 //
 // The running maximum moves only when a score passes it by 2^8, so O (in TMEM) is
-// rarely rescaled; P carries 2^6 more so that fp16 keeps 11 bits down to 2^-20 of
-// the row's largest weight.
+// rarely rescaled, and by whole powers of two, which is exact; P carries 2^6 more so
+// that fp16 keeps 11 bits down to 2^-20 of the row's largest weight.
+//
+// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 771 us, 691
+// TFLOP/s, 42 % of the measured matrix peak; four ragged prompts of up to 2048 tokens,
+// 32 heads: 239 us, 280 TFLOP/s): no unit alone.  A pair of row tiles takes about 6100
+// cycles a key tile; the matrix products and the exponentials need 2048 each, the
+// issue slots 2600 (a third of them the unpacking), and shared memory 3700: the
+// operands of the products 1560, (s, lo) of the keys for eight warps 1280, the
+// unpacked tiles 550.  Prompts lose the rest to tiles on the diagonal and to items of
+// few tiles.  Measured and left out: two threads a row on 16 softmax warps (776 us
+// against 742), 16 x 256-bit TMEM fragments that read (s, lo) a quarter as often (757
+// to 837), the first half of P handed over early (741), maxima from the weights' sums
+// (742), unrolled further (794: the roles share the instruction cache).
 #include <cuda_runtime.h>
 
 #include <atomic>
