@@ -19,9 +19,9 @@
 // because a rounded K would move every score; the pairs act on S instead.  V is
 // rounded like any 16-bit V, which leaves the softmax no work per V row.
 //
-// The key tiles of all (sequence, 256 rows, head) items are one line, cut into equal
-// parts over a persistent grid of one CTA per SM: the load is even whatever the
-// lengths and however few items there are.  The roles run on from item to item: the
+// The key tiles of all (sequence, 256 rows, head) items, and a place for the turn to
+// each, are one line, cut into equal parts over a persistent grid of one CTA per SM:
+// the load is even whatever the lengths and however few items there are.  The roles run on from item to item: the
 // next item's query rows are fetched during the last tile of this one, and its first
 // scores are computed beside this one's last product.  An item cut by a boundary
 // leaves fp32 partial results, joined by a second launch in the order of the parts.
@@ -58,6 +58,7 @@ constexpr int kThreads = 896;  // softmax 0-7, K 8-15, V 16-23, MMA 24, walk 25 
 constexpr int kRows = 256;     // query rows per CTA
 constexpr int kKeys = 128;     // keys per tile
 constexpr int kSeqChunk = 64;  // sequences the search for a CTA's part looks at together
+constexpr int kTurn = 1;       // what the turn to an item costs, in key tiles (6000 cycles: first scores, maximum, result)
 constexpr int kMinTiles = 4;   // key tiles per part: below, joining costs more than the cut spreads
 constexpr float kNegBig = -1e30f;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -85,7 +86,7 @@ struct TileSmem {
   alignas(8) uint8_t hidden[4][8];  // of the tile's records: bit 0: the page is not usable, bit 1: bf16 products with V
   alignas(16) int4 sight[kRows];  // of a row: key j is seen when j < x and (j >= y or j < sinks); z, w: of its row tile
   Item item[kItems];
-  int64_t src[2][32];  // records of four tiles: offset in the pages, -1 beyond the keys, -2 page not usable
+  int64_t src[2][32];  // records of four tiles: offset in the pages, -1 beyond the keys, -2 page not usable, -3 no more tiles
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], par_full[4], s_full[2], p_full[2], o_full[2];
   uint64_t item_full[kItems], item_empty[kItems], src_full[2], src_empty[2], done;
   long long cost[kSeqChunk];
@@ -202,11 +203,12 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-// Key tiles of sequence s over all its blocks and heads (whole warp).
-__device__ __forceinline__ long long seq_tiles(const Kv4AttnArgs &a, int s, int lane) {
+// Length on the line of sequence s over all its blocks and heads (whole warp): an item is kTurn
+// places for the turn to it and a place for each key tile.
+__device__ __forceinline__ long long seq_length(const Kv4AttnArgs &a, int s, int lane) {
   const Rows q = load_rows(a, s);
   long long n = 0;
-  for (int b = lane; b < q.blocks; b += 32) n += keys_of(a, q, b).tiles;
+  for (int b = lane; b < q.blocks; b += 32) n += keys_of(a, q, b).tiles + kTurn;
   return warp_sum(n) * a.c.n_kv;
 }
 
@@ -215,13 +217,21 @@ struct Walk {
   Rows q;
   Keys k;
   int seq, block, head;
-  int t0, t1;  // tiles of the item that belong to the part
-  int left;    // tiles of the part from t0 on
+  int t0, t1;       // tiles of the item that belong to the part
+  int left;         // places of the part from `from` on
+  int from;         // place in the item that the part begins at
+  long long start;  // of the item on the line
 
-  __device__ __forceinline__ void set() { t1 = min(k.tiles, t0 + left); }
+  __device__ __forceinline__ void set() {
+    t0 = max(from - kTurn, 0);
+    t1 = min(k.tiles, max(from + left - kTurn, 0));
+  }
+  __device__ __forceinline__ int length() const { return k.tiles + kTurn; }
+  __device__ __forceinline__ bool more() const { return left - (length() - from) > kTurn; }  // with a tile of it
   __device__ __forceinline__ void next(const Kv4AttnArgs &a) {
-    left -= t1 - t0;
-    t0 = 0;
+    left -= length() - from;
+    start += length();
+    from = 0;
     if (++head == a.c.n_kv) {
       head = 0;
       if (++block >= q.blocks) {
@@ -283,12 +293,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- this CTA's part [lo, lo + mylen) of the line
+  // ---- this CTA's part [lo, lo + span) of the line
   long long total = 0;
   for (int s0 = 0; s0 < a.b.n_seqs; s0 += kSeqChunk) {
     __syncthreads();
     for (int s = warp; s < kSeqChunk; s += kThreads / 32) {
-      const long long c = s0 + s < a.b.n_seqs ? seq_tiles(a, s0 + s, lane) : 0;
+      const long long c = s0 + s < a.b.n_seqs ? seq_length(a, s0 + s, lane) : 0;
       if (lane == 0) sm.cost[s] = c;
     }
     __syncthreads();
@@ -297,17 +307,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   const long long per = (total + gridDim.x - 1) / gridDim.x;
   const long long quota = max(per, static_cast<long long>(kMinTiles));
   const long long lo = min(static_cast<long long>(blockIdx.x) * quota, total);
-  const int mylen = static_cast<int>(min(quota, total - lo));
+  const int span = static_cast<int>(min(quota, total - lo));
   Desc *desc = reinterpret_cast<Desc *>(a.work_tile);
   float *slots = a.work_tile + gridDim.x * (sizeof(Desc) / 4);
   Walk w{};
-  if (mylen > 0) {
+  if (span > 0) {
     long long base = 0;
     for (int s0 = 0; s0 < a.b.n_seqs; s0 += kSeqChunk) {
       if (a.b.n_seqs > kSeqChunk) {  // else the costs are there
         __syncthreads();
         for (int s = warp; s < kSeqChunk; s += kThreads / 32) {
-          const long long c = s0 + s < a.b.n_seqs ? seq_tiles(a, s0 + s, lane) : 0;
+          const long long c = s0 + s < a.b.n_seqs ? seq_length(a, s0 + s, lane) : 0;
           if (lane == 0) sm.cost[s] = c;
         }
         __syncthreads();
@@ -329,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     }
     w.seq = sm.found;
     w.q = load_rows(a, w.seq);
-    // the block: its heads' tiles begin at or before lo and end after it
+    // the block: its heads' places begin at or before lo and end after it
     long long in = lo - sm.found_start, at = 0;
     for (int b0 = 0; b0 < w.q.blocks; b0 += 32) {
-      const long long c = b0 + lane < w.q.blocks ? static_cast<long long>(keys_of(a, w.q, b0 + lane).tiles) * a.c.n_kv : 0;
+      const long long c = b0 + lane < w.q.blocks ? static_cast<long long>(keys_of(a, w.q, b0 + lane).tiles + kTurn) * a.c.n_kv : 0;
       long long incl = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -349,9 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
     w.k = keys_of(a, w.q, w.block);
-    w.head = static_cast<int>(in / w.k.tiles);
-    w.t0 = static_cast<int>(in - static_cast<long long>(w.head) * w.k.tiles);
-    w.left = mylen;
+    w.head = static_cast<int>(in / w.length());
+    w.from = static_cast<int>(in - static_cast<long long>(w.head) * w.length());
+    w.start = lo - w.from;
+    w.left = span;
     w.set();
   }
   tc_fence_before();
@@ -415,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 #pragma unroll 1
     for (int it = 0;; ++it) {
       const Item &x = sm.item[it % kItems], &nx = sm.item[(it + 1) % kItems];  // x has arrived already
-      if (x.n == 0 || sm.dead) break;
+      if (__any_sync(0xffffffffu, x.n == 0 || sm.dead)) break;  // the lanes leave together
       const int n = i ? x.n : x.n0;  // of this row tile
       const bool active = i * 128 < x.rows;
       uint64_t la = f32x2(0.f, 0.f), lb = la;
@@ -628,11 +639,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     uint4 x[D / 64];
     uint32_t pr = 0;    // lane's (s, lo): token lane % 16, of K below lane 16 and V above
     bool gone = false;  // the record's page is not usable
+    bool end = false;   // no more tiles
     auto load = [&](int j) {
-      if (j >= mylen) return;
       const int b = j >> 2;
       if ((j & 3) == 0) wait(&sm.src_full[b & 1], b >> 1 & 1, &sm.dead, a.status);
       const int64_t off = sm.src[b & 1][(j & 3) * 8 + rw];
+      end = __any_sync(0xffffffffu, off == -3 || sm.dead);  // the lanes leave together
       if ((j & 3) == 3) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.src_empty[b & 1]);
@@ -665,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     if (for_k) {
       const float sl2 = a.scale * 1.4426950408889634f;
 #pragma unroll 1
-      for (int j = 0; j < mylen; ++j) {
+      for (int j = 0; !end; ++j) {
         const int st = j & 1;
         const float2 own = kv4_pair<BF>(pr);
         const bool both = finite(own);
@@ -712,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       }
     } else {
 #pragma unroll 1
-      for (int j = 0; j < mylen; ++j) {
+      for (int j = 0; !end; ++j) {
         const int st = j & 1;
         const float2 own = kv4_pair<BF>(pr);
         const bool both = finite(own);
@@ -830,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
           wait(&sm.item_full[slot], (n ? it + 1 : it) / kItems & 1, &sm.dead, a.status);
           next_n = sm.item[slot].n;
           next_n0 = sm.item[slot].n0;
-          next_tiles = next_n == 0 || sm.dead ? 0 : sm.item[slot].rows > 128 ? 2 : 1;
+          next_tiles = __any_sync(0xffffffffu, next_n == 0 || sm.dead) ? 0 : sm.item[slot].rows > 128 ? 2 : 1;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
         }
@@ -887,47 +899,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         ++it;
       };
       Desc d{-1, 0, 0, 0, 0, {}};
-      if (mylen > 0) {
-        publish(false);
+      bool going = span > 0 && w.t1 > w.t0;
+      const bool any = going;
+      if (any) publish(false);
 #pragma unroll 1
-        for (int b = 0; b * 4 < mylen; ++b) {
-          int key = 0, len = 0, seq = 0, head = 0;
+      for (int b = 0; b == 0 || going; ++b) {
+        int key = 0, len = 0, seq = 0, head = 0;
+        bool tile = false;  // the lane's place has one
 #pragma unroll 1
-          for (int x = 0; x < 4 && b * 4 + x < mylen; ++x, ++pj) {
-            if (pj == w.t1 - w.t0) {
+        for (int x = 0; x < 4; ++x, ++pj) {
+          if (going && pj == w.t1 - w.t0) {
+            going = w.more();
+            if (going) {
               w.next(a);
               pj = 0;
               publish(false);
             }
-            if (lane / 8 == x) {
-              key = w.k.key0(w.t0 + pj) + (lane & 7) * 16;
-              len = w.q.len;
-              seq = w.seq;
-              head = w.head;
-            }
           }
-          int64_t off = -1;
-          if (key < len) {
-            const int rec = key / 16;
-            const int slot = a.c.page_shift >= 0 ? rec >> a.c.page_shift : rec / a.c.recs_per_page;
-            const int page = __ldg(a.b.table + seq * a.b.table_stride + slot);
-            if (page < 0 || page >= a.c.n_pages) {
-              off = -2;
-              record_error(a.status, kErrInvalidArg);
-            } else {
-              off = page * a.c.page_stride + (static_cast<int64_t>(head) * a.c.recs_per_page + (rec - slot * a.c.recs_per_page)) * REC;
-            }
+          if (going && lane / 8 == x) {
+            tile = true;
+            key = w.k.key0(w.t0 + pj) + (lane & 7) * 16;
+            len = w.q.len;
+            seq = w.seq;
+            head = w.head;
           }
-          if (b >= 2) wait(&sm.src_empty[b & 1], (b / 2 - 1) & 1, &sm.dead, a.status);
-          sm.src[b & 1][lane] = off;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.src_full[b & 1]);
         }
-        if (w.t0 == 0 && w.t1 < w.k.tiles) {
-          const long long end = lo + mylen + (w.k.tiles - w.t1);
-          d = Desc{static_cast<int>((end - 1) / quota), w.q.row0, w.block * kRows, w.rows(), w.head, {}};
+        int64_t off = tile ? -1 : -3;
+        if (key < len) {
+          const int rec = key / 16;
+          const int slot = a.c.page_shift >= 0 ? rec >> a.c.page_shift : rec / a.c.recs_per_page;
+          const int page = __ldg(a.b.table + seq * a.b.table_stride + slot);
+          if (page < 0 || page >= a.c.n_pages) {
+            off = -2;
+            record_error(a.status, kErrInvalidArg);
+          } else {
+            off = page * a.c.page_stride + (static_cast<int64_t>(head) * a.c.recs_per_page + (rec - slot * a.c.recs_per_page)) * REC;
+          }
         }
+        if (b >= 2) wait(&sm.src_empty[b & 1], (b / 2 - 1) & 1, &sm.dead, a.status);
+        sm.src[b & 1][lane] = off;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.src_full[b & 1]);
       }
+      if (any && w.t0 == 0 && w.t1 < w.k.tiles)
+        d = Desc{static_cast<int>((w.start + w.length() - 1) / quota), w.q.row0, w.block * kRows, w.rows(), w.head, {}};
       publish(true);
       if (lane == 0) desc[blockIdx.x] = d;
     }
