@@ -19,7 +19,7 @@
 // because a rounded K would move every score; the pairs act on S instead.  V is
 // rounded like any 16-bit V, which leaves the softmax no work per V row.
 //
-// The key tiles of all (sequence, 256 rows, head) items, and a place for the turn to
+// The key tiles of all (sequence, 256 rows, head) items, and places for the turn to
 // each, are one line, cut into equal parts over a persistent grid of one CTA per SM:
 // the load is even whatever the lengths and however few items there are.  The roles run on from item to item: the
 // next item's query rows are fetched during the last tile of this one, and its first
@@ -30,9 +30,9 @@
 // rarely rescaled, and by whole powers of two, which is exact; P carries 2^6 more so
 // that fp16 keeps 11 bits down to 2^-20 of the row's largest weight.
 //
-// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 771 us, 691
-// TFLOP/s, 42 % of the measured matrix peak; four ragged prompts of up to 2048 tokens,
-// 32 heads: 239 us, 280 TFLOP/s): no unit alone.  A pair of row tiles takes about 6100
+// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 776 us, 686
+// TFLOP/s, 41 % of the measured matrix peak; four ragged prompts of up to 2048 tokens,
+// 32 heads: 190 us, 353 TFLOP/s): no unit alone.  A pair of row tiles takes about 6100
 // cycles a key tile; the matrix products and the exponentials need 2048 each, the
 // issue slots 2600 (a third of them the unpacking), and shared memory 3700: the
 // operands of the products 1560, (s, lo) of the keys for eight warps 1280, the
@@ -58,7 +58,7 @@ constexpr int kThreads = 896;  // softmax 0-7, K 8-15, V 16-23, MMA 24, walk 25 
 constexpr int kRows = 256;     // query rows per CTA
 constexpr int kKeys = 128;     // keys per tile
 constexpr int kSeqChunk = 64;  // sequences the search for a CTA's part looks at together
-constexpr int kTurn = 1;       // what the turn to an item costs, in key tiles (6000 cycles: first scores, maximum, result)
+constexpr int kTurn = 2;       // what the turn to an item costs, in key tiles (four prompts: 196 us with 1, 189 with 2, 197 with 3)
 constexpr int kMinTiles = 4;   // key tiles per part: below, joining costs more than the cut spreads
 constexpr float kNegBig = -1e30f;
 constexpr uint64_t kWaitNs = 2000000000ull;
