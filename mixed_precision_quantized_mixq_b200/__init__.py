@@ -436,6 +436,7 @@ class KV4Cache:
                                "heads of a page one after another")
         self.pages, self.page_size, self.head_dim, self.dtype = pages, page_size, head_dim, dtype
         self.n_kv_heads, self.device = heads, pages.device
+        self._torch, self._index = torch, pages.get_device()  # -1: not on a GPU
         self._desc = _KV4Desc(pages.data_ptr(), stride if n > 1 else max(1, heads) * per, n,
                               page_size, heads, head_dim, code)
         self._ref = ctypes.addressof(self._desc)
@@ -464,17 +465,16 @@ def _kv4_rows(cache: KV4Cache, name: str, t, heads=None, rows=None):
         raise MixqError(1, f"{name} must have {rows} rows")
     if stride[2] != 1 and n * h * d:
         raise MixqError(1, f"the last dimension of {name} must be contiguous")
-    if t.device != cache.device:
+    if t.get_device() != cache._index:
         raise MixqError(1, f"{name} is on {t.device}, the cache on {cache.device}")
     head = stride[1] if h > 1 else d
     return n, h, stride[0] if n > 1 else max(1, h) * head, head
 
 
 def _kv4_ints(cache: KV4Cache, name: str, t, shape):
-    import torch
-    if t.dtype is not torch.int32 or tuple(t.shape) != shape or (t.stride(-1) != 1 and t.numel() > 1):
+    if t.dtype is not cache._torch.int32 or t.shape != shape or (t.stride(-1) != 1 and t.numel() > 1):
         raise MixqError(1, f"{name} must be contiguous int32 {list(shape)}")
-    if t.device != cache.device:
+    if t.get_device() != cache._index:
         raise MixqError(1, f"{name} is on {t.device}, the cache on {cache.device}")
     return t.data_ptr()
 
@@ -501,21 +501,19 @@ _NOW = contextlib.nullcontext()
 
 def _on(cache: KV4Cache, stream):
     """The cache's device current, and `stream` (if given) the current stream, for a call."""
-    import torch
-    device = cache.device
-    if device.type != "cuda":
+    cuda = cache._torch.cuda
+    if cache._index < 0:
         raise MixqError(6, "the cache must be on an sm_100 GPU")
     if stream is None:
-        return _NOW if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-    if stream.device != device:
-        raise MixqError(1, f"the stream is on {stream.device}, the cache on {device}")
-    return torch.cuda.stream(stream)  # makes its device current too
+        return _NOW if cache._index == cuda.current_device() else cuda.device(cache.device)
+    if stream.device != cache.device:
+        raise MixqError(1, f"the stream is on {stream.device}, the cache on {cache.device}")
+    return cuda.stream(stream)  # makes its device current too
 
 
 def _current_stream(cache: KV4Cache) -> int:
-    import torch
     # what torch.cuda.current_stream(device).cuda_stream says, without the object around it
-    return torch._C._cuda_getCurrentRawStream(cache.device.index)
+    return cache._torch._C._cuda_getCurrentRawStream(cache._index)
 
 
 def kv4_append(k, v, cache: KV4Cache, table, seq_lens, cu_new=None, status=None,
@@ -541,8 +539,7 @@ def kv4_read(cache: KV4Cache, table, cu_rows, rows: int, first=None, k_out=None,
 
     Row cu_rows[s] + i is position first[s] + i of sequence s (first None: from 0; cu_rows None:
     a row each); rows is the number of output rows."""
-    import torch
-    heads = cache.n_kv_heads
+    torch, heads = cache._torch, cache.n_kv_heads
     b = _kv4_batch(cache, table, "first", first, cu_rows, rows)
     with _on(cache, stream):
         if k_out is None:
@@ -564,8 +561,8 @@ def kv4_workspace(cache: KV4Cache, max_rows: int = 0):
     """Scratch for kv4_attention (uint8; calls that may overlap on the GPU must not share one).
 
     max_rows: a bound on new tokens times n_q_heads / n_kv_heads of one sequence (0: none)."""
-    import torch
-    key = (cache.device.index, cache.head_dim, not 0 < max_rows <= _KV4_STEP_ROWS)
+    torch = cache._torch
+    key = (cache._index, cache.head_dim, not 0 < max_rows <= _KV4_STEP_ROWS)
     n = _kv4_work_bytes.get(key)
     if n is None:
         with torch.cuda.device(cache.device):
@@ -583,7 +580,7 @@ def kv4_attention(q, cache: KV4Cache, table, seq_lens, cu_new=None, max_new: int
     window > 0: only the last `window` positions and the first `sinks` ones are seen; work:
     scratch from kv4_workspace (default: allocated for the call).  Returns out [rows,
     n_q_heads, head_dim]; a row that sees no key is zeros."""
-    import torch
+    torch = cache._torch
     rows, heads, q_row, q_head = _kv4_rows(cache, "q", q)
     n, _, at, width, table_row, lens, cu = _kv4_batch(cache, table, "seq_lens", seq_lens, cu_new, rows)
     with _on(cache, stream):
