@@ -67,7 +67,7 @@ size_t kv4_step_workspace(int d, int num_sms);
 size_t kv4_tile_workspace(int d, int num_sms);
 constexpr int kKv4TileAbove = 32;  // more rows (new tokens x group) of a kv head than this: tile kernel
 // Decode steps and small row counts (kv4_attn.cu), many rows (kv4_tile.cu); the
-// first launches the second where it is needed.
+// first launches the second where it is needed, and the join of what both cut (kv4_join.cuh).
 cudaError_t launch_kv4_attn(Kv4AttnArgs a, cudaStream_t stream);
 cudaError_t launch_kv4_tile(const Kv4AttnArgs &a, cudaStream_t stream);
 

@@ -23,8 +23,8 @@
 // over its warps: the load is even whatever the lengths, the host needs to know
 // none of them, and no warp waits for another before its span is done.
 // An item cut between warps is joined in shared memory at the CTA's end; one cut
-// between CTAs leaves fp32 partial results in the workspace, which a second,
-// dependent launch joins in the order of the parts.
+// between CTAs leaves fp32 partial results in the workspace, which a last,
+// dependent launch joins in the order of the parts, those of the tile kernel too.
 //
 // What it measured (B200, warm launches, us against the bytes at the measured copy
 // rate): 16 sequences of up to 4096 tokens, 32 / 32 heads, fp16 50 (30); 64 of up to
@@ -58,9 +58,9 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kUnit = 2;       // records
 constexpr int kUnitKeys = kUnit * kKv4Rec;
 constexpr int kMinQuota = 8;   // units: below one a warp, a cut costs more than it spreads
-constexpr int kMaxRows = 16;
+constexpr int kMaxRows = kKv4StepRows;
 
-__host__ __device__ constexpr size_t slot_floats(int d) { return kMaxRows * static_cast<size_t>(d) + 2 * kMaxRows; }
+__host__ __device__ constexpr size_t slot_floats(int d) { return kv4_slot_floats(kMaxRows, d); }
 
 // What the walk needs to know of a sequence.
 struct Seq {
@@ -788,20 +788,16 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
       mbar_wait(&sm.full[warp][n % SLOTS], n / SLOTS & 1, kWaitNs / 16);
 }
 
-// Joins the parts of the item that starts in part blockIdx.x and ends later, a warp a row.
+// Joins what both kernels cut: first the tile kernel's items (tile_ctas 0: none), then those here.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(R * 32) kv4_join_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Kv4AttnArgs a, int tile_ctas, int ctas) {
   griddep_wait();
   griddep_launch_dependents();
-  const Kv4Join x = reinterpret_cast<const Kv4Join *>(a.work)[blockIdx.x];
-  const int r = threadIdx.x / 32, c0 = blockIdx.x;
-  if (x.last < 0 || r >= x.rows) return;
-  const float *slots = a.work + gridDim.x * (sizeof(Kv4Join) / 4);
-  auto part = [&](int c) { return slots + (2 * static_cast<size_t>(c) + (c == c0)) * slot_floats(D); };
-  const int rr = x.first + r, qi = rr / a.group;
-  kv4_join_row<D>(part, c0, x.last, kMaxRows, r, threadIdx.x & 31,
-                  static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
-                      (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head);
+  const int i = blockIdx.x * kWarps + threadIdx.x / 32, tiles = tile_ctas * (kKv4TileRows / 4);
+  if (i < tiles)
+    kv4_join<D, kKv4TileRows, 4, T>(a, a.work_tile, tile_ctas, i, kKv4TileRows / 4);
+  else if (i - tiles < ctas * R)
+    kv4_join<D, kMaxRows, 1, T>(a, a.work, ctas, i - tiles, R);
 }
 
 template <typename T, int D, int R>
@@ -824,9 +820,10 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
-  cfg.blockDim = dim3(R * 32, 1, 1);
+  const int ctas = cfg.gridDim.x, tile_ctas = a.tile_above < INT64_MAX ? a.num_sms : 0;
+  cfg.gridDim = dim3((tile_ctas * (kKv4TileRows / 4) + ctas * R + kWarps - 1) / kWarps, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D, R>, a);
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D, R>, a, tile_ctas, ctas);
 }
 
 template <typename T, int D>

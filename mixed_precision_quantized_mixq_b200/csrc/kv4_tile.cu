@@ -24,15 +24,15 @@
 // the load is even whatever the lengths and however few items there are.  The roles run on from item to item: the
 // next item's query rows are fetched during the last tile of this one, and its first
 // scores are computed beside this one's last product.  An item cut by a boundary
-// leaves fp32 partial results, joined by a second launch in the order of the parts.
+// leaves fp32 partial results, which the call's last launch joins in their order.
 //
 // The running maximum moves only when a score passes it by 2^8, so O (in TMEM) is
 // rarely rescaled, and by whole powers of two, which is exact; P carries 2^6 more so
 // that fp16 keeps 11 bits down to 2^-20 of the row's largest weight.
 //
-// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 776 us, 686
-// TFLOP/s, 41 % of the measured matrix peak; four ragged prompts of up to 2048 tokens,
-// 32 heads: 190 us, 353 TFLOP/s): no unit alone.  A pair of row tiles takes about 6100
+// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 766 us, 695
+// TFLOP/s, 42 % of the measured matrix peak; four ragged prompts of up to 2048 tokens,
+// 32 heads: 187 us, 358 TFLOP/s): no unit alone.  A pair of row tiles takes about 6100
 // cycles a key tile; the matrix products and the exponentials need 2048 each, the
 // issue slots 2600 (a third of them the unpacking), and shared memory 3700: the
 // operands of the products 1560, (s, lo) of the keys for eight warps 1280, the
@@ -55,7 +55,7 @@ namespace mixq {
 namespace {
 
 constexpr int kThreads = 896;  // softmax 0-7, K 8-15, V 16-23, MMA 24, walk 25 (26, 27 complete its group)
-constexpr int kRows = 256;     // query rows per CTA
+constexpr int kRows = kKv4TileRows;  // query rows per CTA
 constexpr int kKeys = 128;     // keys per tile
 constexpr int kSeqChunk = 64;  // sequences the search for a CTA's part looks at together
 constexpr int kTurn = 2;       // what the turn to an item costs, in key tiles (four prompts: 196 us with 1, 189 with 2, 197 with 3)
@@ -249,7 +249,7 @@ struct Walk {
 
 using Desc = Kv4Join;
 
-__host__ __device__ constexpr size_t slot_floats(int d) { return kRows * (static_cast<size_t>(d) + 2); }
+__host__ __device__ constexpr size_t slot_floats(int d) { return kv4_slot_floats(kRows, d); }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs a) {
@@ -954,26 +954,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   }
 }
 
-// Joins the parts of the item that starts in part blockIdx.x and ends later: a warp a row, kJoin
-// rows a block.
-constexpr int kJoin = 32;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoin * 32) kv4_tile_join_kernel(const Kv4AttnArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const Desc x = reinterpret_cast<const Desc *>(a.work_tile)[blockIdx.x];
-  const int r = blockIdx.y * kJoin + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (x.last < 0 || r >= x.rows) return;
-  const float *slots = a.work_tile + gridDim.x * (sizeof(Desc) / 4);
-  const int c0 = blockIdx.x;
-  auto part = [&](int c) { return slots + (2 * static_cast<size_t>(c) + (c == c0)) * slot_floats(D); };
-  const int rr = x.first + r, qi = rr / a.group;
-  kv4_join_row<D>(part, c0, x.last, kRows, r, lane,
-                  static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
-                      (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head);
-}
-
 template <typename T, int D>
 cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   auto kernel = kv4_tile_kernel<T, D>;
@@ -991,12 +971,7 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.num_sms, kRows / kJoin, 1);
-  cfg.blockDim = dim3(kJoin * 32, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv4_tile_join_kernel<T, D>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace

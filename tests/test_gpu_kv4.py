@@ -326,6 +326,8 @@ CHUNK = [
     ([257], [257], 2, 2, 64, 48, BF16),
     ([700, 20], [140, 20], 5, 5, 128, 64, F16),
     ([500, 1], [4, 1], 16, 2, 128, 64, BF16),
+    ([3100], [40], 2, 1, 64, 32, F16),    # one item over more CTAs than a join takes at once
+    ([2600], [90], 3, 1, 128, 64, BF16),
 ]
 
 
