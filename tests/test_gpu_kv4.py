@@ -337,6 +337,34 @@ def test_chunks(lens, new, heads, n_kv, D, page, dtype, hint):
     attend(12, lens, new, heads, n_kv, D, page, dtype, max_new=max(new) if hint else 0, pad=3)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_ragged_batches_of_prompts_on_both_kernels(dtype, D):
+    """Batches whose blocks fill one row tile here and two there, so that a CTA takes both kinds in a row, against the
+    kernel for few rows (which takes all of them under a wrong hint).  Either result is within half a step of the type
+    of its own value, and weights and V rows are rounded once each to at least the type: for outputs and V rows of at
+    most vmax that is 4 half steps of vmax.  Scratch and shared memory hold other calls' bytes between the runs."""
+    n_kv, heads, page = 4, 12, 64
+    g = torch.Generator().manual_seed(31)
+    junk = mq.KV4Cache(torch.full((40, n_kv, page * (D + 8)), 255, dtype=torch.uint8, device="cuda"), page, D, dtype)
+    step = torch.finfo(dtype).eps / 2
+    for trial in range(12):
+        new = torch.randint(1, 420, (9,), generator=g).tolist()
+        new[trial % 9], new[(trial + 4) % 9] = 12, 900
+        lens = [n + int(x) for n, x in zip(new, torch.randint(0, 40, (9,), generator=g))]
+        pages, table, _ = make(40 + trial, lens, n_kv, D, page, dtype)
+        cache, t, cu = mq.KV4Cache(pages.cuda(), page, D, dtype), table.cuda(), ints(offsets(new))
+        q = randn(g, (sum(new), heads, D), dtype).cuda()
+        want = mq.kv4_attention(q, cache, t, ints(lens), cu, max_new=1).float()
+        _, v = mq.kv4_read(cache, t, ints(offsets(lens)), sum(lens))
+        for _ in range(4):
+            few = torch.arange(40, dtype=torch.int32, device="cuda").view(4, 10)
+            mq.kv4_attention(q[:240], junk, few, ints([640] * 4), ints([0, 60, 120, 180, 240]))  # NaN pairs everywhere
+            got = mq.kv4_attention(q, cache, t, ints(lens), cu).float()
+            off = (got - want).abs().max().item() / v.float().abs().max().item()
+            assert off <= 4 * step + 1e-5, (trial, off)
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (7, 0), (16, 4), (17, 3), (100, 20), (64, 64), (90, 500), (1000, 4)])
 @pytest.mark.parametrize("new", [None, [1, 40, 129], [3, 2, 5]])
 def test_windows(window, sinks, new):
