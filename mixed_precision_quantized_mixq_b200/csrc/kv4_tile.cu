@@ -379,6 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes per warp
     int jt = 0;  // key tiles of the CTA so far
     int jn = 0;  // those of this row tile (its barriers' phases)
+    // After items that had nothing for this row tile it is ahead of the keys, and the phase of their
+    // barrier then says nothing (two phases back looks like done).
+    bool ahead = false;
     float qsum = 0.f;
     // The warp's 32 query rows of an item into the operand tile, D/8 lanes a row; then, once they
     // are there, each lane's sum over its own row.
@@ -446,15 +449,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int st = (jt + j) & 3;
-          wait(&sm.s_full[i], (jn + j) & 1, &sm.dead, a.status);
-          // Only now: a row tile that had nothing in the items before is ahead of the keys, and this
-          // barrier's phase then says nothing (two phases back looks like done).
+          if (ahead) {  // the keys are there when the scores are
+            wait(&sm.s_full[i], jn & 1, &sm.dead, a.status);
+            ahead = false;
+          }
           wait(&sm.par_full[st], ((jt + j) >> 2) & 1, &sm.dead, a.status);
           const float4 *kp = sm.kp[st];
           const uint2 hid = *reinterpret_cast<const uint2 *>(sm.hidden[st]);
           const int k0 = (x.t0 + j + (x.t0 + j >= x.sinks ? x.skip : 0)) * kKeys;
           const bool whole = ((hid.x | hid.y) & 0x01010101u) == 0 && k0 + kKeys <= sm.sight[r].z &&
                              (a.window <= 0 || k0 > sm.sight[r].w - a.window || k0 + kKeys <= a.sinks);
+          wait(&sm.s_full[i], (jn + j) & 1, &sm.dead, a.status);
           tc_fence_after();
           if (j + 1 == n) {  // the last scores are there, so the operand tile is free for the next rows
             wait(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
@@ -585,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         }
         jn += n;
       } else {
+        ahead = true;
         wait(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
         if (nx.n > 0) fetch_q(nx);
       }
