@@ -30,9 +30,9 @@
 // rarely rescaled, and by whole powers of two, which is exact; P carries 2^6 more so
 // that fp16 keeps 11 bits down to 2^-20 of the row's largest weight.
 //
-// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 766 us, 695
+// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 773 us, 689
 // TFLOP/s, 42 % of the measured matrix peak; four ragged prompts of up to 2048 tokens,
-// 32 heads: 187 us, 358 TFLOP/s): no unit alone.  A pair of row tiles takes about 6100
+// 32 heads: 188 us, 356 TFLOP/s): no unit alone.  A pair of row tiles takes about 6100
 // cycles a key tile; the matrix products and the exponentials need 2048 each, the
 // issue slots 2600 (a third of them the unpacking), and shared memory 3700: the
 // operands of the products 1560, (s, lo) of the keys for eight warps 1280, the
@@ -40,7 +40,8 @@
 // few tiles.  Measured and left out: two threads a row on 16 softmax warps (776 us
 // against 742), 16 x 256-bit TMEM fragments that read (s, lo) a quarter as often (757
 // to 837), the first half of P handed over early (741), maxima from the weights' sums
-// (742), unrolled further (794: the roles share the instruction cache).
+// (742), unrolled further (794: the roles share the instruction cache), the next chunk's
+// scores computed beside this one's exponentials (783 against 773).
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             uint32_t u[32];
             float f[32];
             uint64_t d[16];
-          } buf[2];
+          };
           // t + base of 32 keys in place of their scores, and the largest
           auto scores = [&](Chunk &t, int c) -> float {
             const uint64_t b2 = f32x2(base, base);
@@ -538,35 +539,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             }
             tmem_st_wait();
           };
-          // 32 keys at a time: the exponentials of one chunk beside the scores of the next.  P of
-          // keys [32c, 32c + 32) takes TMEM columns [16c, 16c + 16), whose scores have been read.
-          tmem_ld32(tm_s(i) + lanes, buf[0].u);
-          tmem_ld_wait();
-          tmem_ld32(tm_s(i) + lanes + 32, buf[1].u);
-          float mx = scores(buf[0], 0);
-          // not unrolled further: the roles share the instruction cache
-#pragma unroll 1
-          for (int c0 = 0; c0 < 4; c0 += 2) {
+          // 32 keys at a time.  P of keys [32c, 32c + 32) takes TMEM columns [16c, 16c + 16), whose
+          // scores have been read.  Not unrolled further: the roles share the instruction cache.
+#pragma unroll 2
+          for (int c = 0; c < 4; ++c) {
+            Chunk t;
+            tmem_ld32(tm_s(i) + lanes + c * 32, t.u);
+            tmem_ld_wait();
+            const float mx = scores(t, c);
+            if (__builtin_expect(__any_sync(0xffffffffu, mx > limit), 0)) grow(t, c, mx);
+            uint32_t p[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c = c0 + h;
-              const bool next = h == 0 || c0 == 0;
-              Chunk &t = buf[h];
-              if (__builtin_expect(__any_sync(0xffffffffu, mx > limit), 0)) grow(t, c, mx);
-              if (next) tmem_ld_wait();
-              uint32_t p[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 x = from_f32x2(t.d[e]);
-                const float p0 = ex2f(x.x), p1 = ex2f(x.y);
-                if (e & 1) lb = add_f32x2(lb, f32x2(p0, p1));
-                else la = add_f32x2(la, f32x2(p0, p1));
-                p[e] = kv4_bits<uint32_t>(__floats2half2_rn(p0, p1));
-              }
-              if (next) mx = scores(buf[h ^ 1], c + 1);
-              tmem_st16(tm_s(i) + lanes + c * 16, p);
-              if (c0 == 0) tmem_ld32(tm_s(i) + lanes + (c + 2) * 32, t.u);
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = from_f32x2(t.d[e]);
+              const float p0 = ex2f(y.x), p1 = ex2f(y.y);
+              if (e & 1) lb = add_f32x2(lb, f32x2(p0, p1));
+              else la = add_f32x2(la, f32x2(p0, p1));
+              p[e] = kv4_bits<uint32_t>(__floats2half2_rn(p0, p1));
             }
+            tmem_st16(tm_s(i) + lanes + c * 16, p);
           }
           tmem_st_wait();
           if (BF && __builtin_expect((hid.x | hid.y) & 0x02020202u, 0)) {  // weights of bf16 products
