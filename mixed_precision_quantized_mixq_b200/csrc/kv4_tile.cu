@@ -21,10 +21,11 @@
 //
 // The key tiles of all (sequence, 256 rows, head) items, and places for the turn to
 // each, are one line, cut into equal parts over a persistent grid of one CTA per SM:
-// the load is even whatever the lengths and however few items there are.  The roles run on from item to item: the
-// next item's query rows are fetched during the last tile of this one, and its first
-// scores are computed beside this one's last product.  An item cut by a boundary
-// leaves fp32 partial results, which the call's last launch joins in their order.
+// the load is even whatever the lengths and however few items there are.  The roles
+// run on from item to item: the next item's query rows are fetched during the last
+// tile of this one, and its first scores are computed beside this one's last product.
+// An item cut by a boundary leaves fp32 partial results, which the call's last launch
+// joins in their order.
 //
 // The running maximum moves only when a score passes it by 2^8, so O (in TMEM) is
 // rarely rescaled, and by whole powers of two, which is exact; P carries 2^6 more so
