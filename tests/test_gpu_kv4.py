@@ -604,6 +604,41 @@ def test_streams_and_capture():
     assert n.cpu().tolist() == [50, 100]
 
 
+def test_chunks_captured_and_on_two_streams():
+    """A captured chunk replayed with other lengths and offsets, some sequences with one row and some with many, and
+    the same call on two streams at once; against the kernel for few rows under a wrong hint, within the same 4 half
+    steps of vmax as above."""
+    D, page, n_kv, heads = 128, 32, 2, 8
+    pages, table, g = make(33, [700] * 5, n_kv, D, page, F16)
+    cache, t = mq.KV4Cache(pages.cuda(), page, D, F16), table.cuda()
+    vmax = mq.kv4_read(cache, t, ints(offsets([700] * 5)), 3500)[1].float().abs().max().item()
+    rows = 640
+    q = randn(g, (rows, heads, D), F16).cuda()
+    out = torch.zeros_like(q)
+    lens, cu = ints([0] * 5), ints([0] * 6)
+    work = mq.kv4_workspace(cache)
+    mq.kv4_attention(q, cache, t, lens, cu, out=out, work=work)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mq.kv4_attention(q, cache, t, lens, cu, out=out, work=work)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for new, full in (([300, 1, 200, 0, 139], [600, 700, 200, 5, 333]), ([1, 1, 1, 1, 1], [700, 20, 333, 1, 64]),
+                      ([128, 129, 127, 256, 0], [128, 640, 700, 300, 0])):
+        cu.copy_(ints(offsets(new)))
+        lens.copy_(ints(full))
+        n = sum(new)
+        out.fill_(7.0)
+        graph.replay()
+        want = mq.kv4_attention(q, cache, t, lens, cu, max_new=1)
+        assert (out[:n].float() - want[:n].float()).abs().max().item() <= (4 * 2.0 ** -11 + 1e-5) * vmax
+        assert bool((out[n:] == 7).all())
+        torch.cuda.synchronize()
+        both = [mq.kv4_attention(q, cache, t, lens, cu, stream=s) for s in streams for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o[:n], out[:n]) for o in both)
+
+
 def test_offsets_past_32_bits():
     """Pages beyond 4 GiB from the start of the pool."""
     D, page, n_kv = 128, 128, 8
