@@ -411,7 +411,8 @@ mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_ro
  * cache); with more rows the weights and V's rows are rounded to fp16 for their
  * product (to bf16 for 16 tokens of a bf16 cache whose V values do not fit fp16).
  * A row that sees no key is written as zeros; a NaN in a row reaches only those
- * queries that see the row.
+ * queries that see the row.  A result above the type's largest finite value in size
+ * becomes that.  V rows of up to 2^90 in size are safe from overflow in the sums.
  *   q, out   [n_rows][n_q_heads][head_dim], strides in elements, multiples of 8;
  *            16-byte aligned; out must not overlap q
  *   max_new  a bound on cu[s+1] - cu[s], or 0 for none: it picks the kernel, the

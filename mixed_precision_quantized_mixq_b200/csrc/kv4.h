@@ -102,6 +102,13 @@ struct Kv4Type<__half> {
   static constexpr bool bf16 = false;
   static __device__ __forceinline__ float2 f2(__half2 v) { return __half22float2(v); }
   static __device__ __forceinline__ __half2 from2(float a, float b) { return __floats2half2_rn(a, b); }
+  // the same, but held at the largest finite value (NaN stays): outputs of attention.  A mean of V rows
+  // can pass it, as 15 s + lo can (s is rounded) and as rounded weights need not sum to what divides them.
+  static __device__ __forceinline__ uint32_t held2(float a, float b) {
+    uint32_t d;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+  }
   static constexpr float max_finite = 65504.f;
 };
 template <>
@@ -111,6 +118,11 @@ struct Kv4Type<__nv_bfloat16> {
   static __device__ __forceinline__ float2 f2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
   static __device__ __forceinline__ __nv_bfloat162 from2(float a, float b) {
     return __floats2bfloat162_rn(a, b);
+  }
+  static __device__ __forceinline__ uint32_t held2(float a, float b) {
+    uint32_t d;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
   }
   static constexpr float max_finite = 3.3895313892515355e38f;
 };

@@ -703,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
                   (static_cast<int64_t>(head) * a.group + (rr - qi * a.group)) * a.o_head + 2 * g;
 #pragma unroll
           for (int i = 0; i < MT; ++i)
-            *reinterpret_cast<uint32_t *>(op + 16 * i) = kv4_bits<uint32_t>(
-                Kv4Type<T>::from2(fmaf(o[nt][i][j] * 16777216.f, un, zj) * inv, fmaf(o[nt][i][j + 2] * 1048576.f, un, zj) * inv));
+            *reinterpret_cast<uint32_t *>(op + 16 * i) =
+                Kv4Type<T>::held2(fmaf(o[nt][i][j] * 16777216.f, un, zj) * inv, fmaf(o[nt][i][j + 2] * 1048576.f, un, zj) * inv);
         } else {
 #pragma unroll
           for (int i = 0; i < MT; ++i)
@@ -770,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
                 (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head + d;
         using X = Kv4Type<T>;
         uint2 v;
-        v.x = kv4_bits<uint32_t>(X::from2(acc.x * inv, acc.y * inv));
-        v.y = kv4_bits<uint32_t>(X::from2(acc.z * inv, acc.w * inv));
+        v.x = X::held2(acc.x * inv, acc.y * inv);
+        v.y = X::held2(acc.z * inv, acc.w * inv);
         *reinterpret_cast<uint2 *>(op) = v;
       } else {
         *reinterpret_cast<float4 *>(part + r * D + d) = acc;

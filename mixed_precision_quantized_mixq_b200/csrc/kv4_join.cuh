@@ -66,7 +66,7 @@ __device__ __forceinline__ void kv4_join_row(F part, int c0, int last, int r, in
 #pragma unroll
   for (int i = 0; i < V; i += 2)
     *reinterpret_cast<uint32_t *>(op + lane * V + i) =
-        kv4_bits<uint32_t>(Kv4Type<T>::from2(acc[i] * inv, acc[i + 1] * inv));
+        Kv4Type<T>::held2(acc[i] * inv, acc[i + 1] * inv);
 }
 
 // Joins the items of `ctas` CTAs that were cut, N rows a warp, parts in their order.  A CTA has two
@@ -128,7 +128,7 @@ __device__ __forceinline__ void kv4_join(const Kv4AttnArgs &a, const float *work
       T *op = place(r0 + n) + lane * V;
 #pragma unroll
       for (int v = 0; v < V; v += 2)
-        *reinterpret_cast<uint32_t *>(op + v) = kv4_bits<uint32_t>(Kv4Type<T>::from2(acc[n][v] * inv, acc[n][v + 1] * inv));
+        *reinterpret_cast<uint32_t *>(op + v) = Kv4Type<T>::held2(acc[n][v] * inv, acc[n][v + 1] * inv);
     }
     return;
   }

@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
               uint32_t y[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z)
-                y[z] = kv4_bits<uint32_t>(X::from2(__uint_as_float(e0[4 * e + z]) * inv, __uint_as_float(e1[4 * e + z]) * inv));
+                y[z] = X::held2(__uint_as_float(e0[4 * e + z]) * inv, __uint_as_float(e1[4 * e + z]) * inv);
               reinterpret_cast<uint4 *>(op)[c * 4 + e] = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else if (valid) {

@@ -38,3 +38,36 @@ def test_pairs_behind_the_last_token_may_be_any_bytes(dtype, s, lo, new, D):
 
     out, _ = attend(53, lens, new, 8, 2, D, page, dtype, prepare=rest)
     assert bool(torch.isfinite(out).all())
+
+
+# ------------------------------------------------------------ the type's largest values
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [None, [20, 150]])
+def test_rows_that_reach_the_largest_value(new, D):
+    """fp16 V rows up to +-65504: s is rounded, so 15 s + lo can be above it, and is held there as in reading back.  Each
+    query sees one key (window 1), then all.  With one key the weights cancel but for their own rounding on the kernel
+    for many rows (2^-12 of the weight and 2^-12 of the result); 2^-10 of 65504 is twice their sum."""
+    page, n_kv, lens, top = 16, 2, [40, 150], 65504.0
+    g = torch.Generator().manual_seed(54)
+    pages, table, _ = make(54, lens, n_kv, D, page, F16)
+    n = sum(lens)
+    v = torch.rand((n, n_kv, D), generator=g) * 1000
+    v[:, 0, 3], v[:, 1, D - 1] = top, top
+    v[:, :, 7] = -torch.arange(n)[:, None] * 97.0  # lo, of every residue
+    v[::3, :, 9] = -top
+    k, v = randn(g, v.shape, F16), v.half()
+    over = ref.quantize(v)
+    assert bool((15 * over[1].double() + over[2].double() >= 65520).any())  # rounds to infinity
+    cache, t, cu_all = mq.KV4Cache(pages.cuda(), page, D, F16), table.cuda(), ints(offsets(lens))
+    mq.kv4_append(k.cuda(), v.cuda(), cache, t, ints(lens), cu_all)
+    _, back = mq.kv4_read(cache, t, cu_all, n)
+    assert bool(torch.isfinite(back).all())
+    rows = [1, 1] if new is None else new
+    q = randn(g, (sum(rows), 2 * n_kv, D), F16)
+    cu = None if new is None else ints(offsets(rows))
+    one = mq.kv4_attention(q.cuda(), cache, t, ints(lens), cu, window=1)
+    every = mq.kv4_attention(q.cuda(), cache, t, ints(lens), cu)
+    assert bool(torch.isfinite(one).all()) and bool(torch.isfinite(every).all())
+    at = [offsets(lens)[s] + lens[s] - rows[s] + i for s in range(2) for i in range(rows[s])]
+    want = back[at].repeat_interleave(2, 1).float()
+    assert (one.float() - want).abs().max().item() <= 2.0 ** -10 * top
