@@ -72,8 +72,9 @@ struct Seq {
   int skip_at, skip_by;  // unit index i >= skip_at means unit i + skip_by
 };
 
+// wrong: set if the sequence's offsets or length are not usable
 template <int R>
-__device__ __forceinline__ Seq load_seq(const Kv4AttnArgs &a, int s) {
+__device__ __forceinline__ Seq load_seq(const Kv4AttnArgs &a, int s, bool *wrong = nullptr) {
   Seq q{};
   bool bad = false;
   const int2 r = kv4_row_range(a.b, s, &bad);
@@ -82,9 +83,7 @@ __device__ __forceinline__ Seq load_seq(const Kv4AttnArgs &a, int s) {
   const int full = __ldg(a.b.lens + s);
   const int64_t cap = static_cast<int64_t>(a.b.table_width) * a.c.recs_per_page * kKv4Rec;
   q.len = static_cast<int>(min(static_cast<int64_t>(max(full, 0)), cap));
-  if (bad || full < 0 || full > cap) {
-    if (threadIdx.x == 0) record_error(a.status, kErrInvalidArg);
-  }
+  if (wrong) *wrong = bad || full < 0 || full > cap;
   q.pos0 = full - q.nq;
   const int64_t rows = static_cast<int64_t>(q.nq) * a.group;
   q.tiles = rows > a.tile_above ? 0 : static_cast<int>((rows + R - 1) / R);
@@ -199,7 +198,10 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
   long long total = 0, cost = 0, start = 0;  // of the thread's last sequence
   auto scan = [&](int s0) {
     const int s = s0 + tid;
-    cost = s < a.b.n_seqs ? seq_cost(load_seq<R>(a, s), a.c.n_kv) : 0;
+    bool wrong = false;
+    cost = s < a.b.n_seqs ? seq_cost(load_seq<R>(a, s, &wrong), a.c.n_kv) : 0;
+    // here, where every sequence is looked at, those without work too
+    if (wrong && blockIdx.x == 0) record_error(a.status, kErrInvalidArg);
     long long incl = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

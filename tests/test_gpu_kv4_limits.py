@@ -19,6 +19,55 @@ def env():
     mq.lib()
 
 
+# ------------------------------------------------- bad sequences among good ones
+@pytest.mark.parametrize("lens", [[16, 49], [40, 49], [49, 40], [30, 20, 10, 48, 49], [3] * 299 + [49], [3] * 299 + [-1],
+                                  [49] + [3] * 299, [3] * 260 + [49] + [3] * 300])
+@pytest.mark.parametrize("group", [1, 40])
+def test_a_bad_length_is_reported_wherever_it_is(lens, group):
+    """A length that the table (48 tokens) cannot hold, or a negative one, at any place of a batch; rows of a kv head on
+    the kernel for few rows (1) and on the one for many (40)."""
+    D, page, n_kv = 64, 16, 2
+    good = [n if 0 <= n <= 48 else 48 for n in lens]
+    pages, table, g = make(51, good, n_kv, D, page, F16, width=3)
+    cache = mq.KV4Cache(pages.cuda(), page, D, F16)
+    q = randn(g, (len(lens), n_kv * group, D), F16)
+    status = mq.status_tensor()
+    mq.kv4_attention(q.cuda(), cache, table.cuda(), ints(good), status=status)
+    mq.check_status(status)
+    out = mq.kv4_attention(q.cuda(), cache, table.cuda(), ints(lens), status=status)
+    assert int(status.item()) == 1
+    first = [i for i, (a, b) in enumerate(zip(lens, good)) if a == b][:4]
+    want, tol = ref.attention(ref.Pages(pages, page, D, F16), q[first], table[first], [good[i] for i in first], None, D ** -0.5)
+    ref.assert_close(out[first], want, tol)
+
+
+@pytest.mark.parametrize("cu", [[0, 2, 4, 3], [0, 2, 4, 7], [0, 2, -1, 4], [0, 4, 2, 4], [-1, 2, 3, 4], [0, 0, 0, 1 << 30],
+                                list(range(300)) + [298], [0] * 299 + [300, 299]])
+@pytest.mark.parametrize("hint", [1, 0])
+def test_bad_offsets_are_reported_by_attention(cu, hint):
+    """Offsets that fall or leave the rows, at any place of a batch, by the kernel for few rows alone (hint 1) and by
+    both.  Sequences that are in order and share no row with others keep their results."""
+    D, page, n_kv, heads = 64, 16, 2, 24
+    n, rows = len(cu) - 1, max(4, min(len(cu) - 1, 300))
+    lens = [20] * n
+    pages, table, g = make(52, lens, n_kv, D, page, F16)
+    cache = mq.KV4Cache(pages.cuda(), page, D, F16)
+    q = randn(g, (rows, heads, D), F16)
+    status = mq.status_tensor()
+    out = torch.full(q.shape, 5.0, dtype=F16, device="cuda")
+    mq.kv4_attention(q.cuda(), cache, table.cuda(), ints(lens), ints(cu), max_new=hint, out=out, status=status)
+    assert int(status.item()) == 1
+    good = [s for s in range(n) if 0 <= cu[s] <= cu[s + 1] <= rows]
+    owners = [sum(cu[s] <= r < cu[s + 1] for s in good) for r in range(rows)]
+    assert all(bool((out[r] == 5).all()) for r in range(rows) if owners[r] == 0)
+    host = ref.Pages(pages, page, D, F16)
+    for s in [s for s in good if cu[s + 1] > cu[s]][:3]:
+        r = range(cu[s], cu[s + 1])
+        if all(owners[i] == 1 for i in r):
+            want, tol = ref.attention(host, q[r.start:r.stop], table[s:s + 1], lens[s:s + 1], [0, len(r)], D ** -0.5)
+            ref.assert_close(out[r.start:r.stop], want, tol, f"sequence {s}")
+
+
 # ------------------------------------------------------- bytes that no token wrote
 @pytest.mark.parametrize("dtype,s,lo", [(F16, -60000.0, -60000.0), (F16, -5000.0, 0.0), (F16, 60000.0, 60000.0),
                                         (BF16, -1e38, -1e38), (BF16, -3e37, 0.0), (BF16, 1e38, 1e38)])
