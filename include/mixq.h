@@ -352,7 +352,9 @@ mixq_status mixq_gemm_plan(int mode, int M, int N, int K, int num_sms, int *bn, 
  * device reports MIXQ_ERR_INVALID_ARG in *status for a page number outside
  * [0, n_pages) or beyond table_width (those tokens are not stored, read back as
  * they were, and are hidden from attention) and for a cu that falls or leaves
- * [0, n_rows] (such a sequence counts as empty).  Table entries that no
+ * [0, n_rows] (such a sequence counts as empty).  After a cu that falls, append and
+ * read may leave out rows of the call's other sequences, and attention may write rows
+ * that two ranges share for either; nothing else is touched.  Table entries that no
  * position in use needs are not read.
  */
 enum { MIXQ_KV4_F16 = 0, MIXQ_KV4_BF16 = 1 };

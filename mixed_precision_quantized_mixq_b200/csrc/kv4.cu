@@ -51,6 +51,16 @@ __device__ __forceinline__ int find_seq(const Kv4Batch &b, int v, int lane) {
   return lo;
 }
 
+// The first blocks of a call with offsets look at all of them, a sequence a thread: offsets that fall
+// may hide a sequence from the search.  Blocks of their own, as values held beside the search cost
+// the others registers (prefixes 65 -> 68 us).
+__device__ __forceinline__ void check_offsets(const Kv4Batch &b, int32_t *status) {
+  const unsigned s = blockIdx.x * (kWarps * 32) + threadIdx.x;
+  bool bad = false;
+  if (blockIdx.y == 0 && s < b.n_seqs) kv4_row_range(b, s, &bad);
+  if (bad) record_error(status, kErrInvalidArg);
+}
+
 struct Place {
   int row0;       // row of the record's token 0 (may lie before the range)
   int t0, t1;     // tokens [t0, t1) of the record belong to the call
@@ -191,14 +201,15 @@ __device__ __forceinline__ uint32_t quantize8(const uint4 &raw, uint32_t *pair) 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32, 4)
-    kv4_append_kernel(Kv4Cache c, Kv4Batch b, Kv4Rows r, int32_t *status) {
+    kv4_append_kernel(Kv4Cache c, Kv4Batch b, Kv4Rows r, int32_t *status, unsigned checks) {
   constexpr int LANES = D / 8, RPW = 32 / LANES;  // lanes per row, rows per warp load
   griddep_wait();
   griddep_launch_dependents();
+  if (blockIdx.x < checks) return check_offsets(b, status);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int h = blockIdx.y * kWarps + warp;
   if (h >= c.n_kv) return;
-  const Place p = locate(c, b, blockIdx.x, lane, true, status);
+  const Place p = locate(c, b, blockIdx.x - checks, lane, true, status);
   if (p.t0 >= p.t1) return;
   const int sub = lane / LANES, l = lane % LANES;
   uint8_t *rec = nullptr;
@@ -289,15 +300,16 @@ __device__ __forceinline__ uint4 dequantize8(uint32_t w, float2 sl) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32, 5)
-    kv4_read_kernel(Kv4Cache c, Kv4Batch b, Kv4Rows r, int32_t *status) {
+    kv4_read_kernel(Kv4Cache c, Kv4Batch b, Kv4Rows r, int32_t *status, unsigned checks) {
   constexpr int LANES = D / 8, RPW = 32 / LANES;
   constexpr bool BF = Kv4Type<T>::bf16;
   griddep_wait();
   griddep_launch_dependents();
+  if (blockIdx.x < checks) return check_offsets(b, status);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int h = blockIdx.y * kWarps + warp;
   if (h >= c.n_kv) return;
-  const Place p = locate(c, b, blockIdx.x, lane, false, status);
+  const Place p = locate(c, b, blockIdx.x - checks, lane, false, status);
   if (p.t0 >= p.t1) return;
   const int sub = lane / LANES, l = lane % LANES;
   const uint8_t *rec = record(c, p, lane, status);
@@ -339,9 +351,10 @@ template <typename K>
 cudaError_t launch(K kernel, const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows &r,
                    int32_t *status, cudaStream_t stream) {
   // virtual records: one per sequence, or the last start plus the last sequence's own
-  const int64_t n = b.cu ? static_cast<int64_t>(b.rows / 16) + 2ll * b.n_seqs : b.n_seqs;
+  const unsigned records = b.cu ? b.rows / 16 + 2u * b.n_seqs : b.n_seqs;
+  const unsigned checks = b.cu ? (b.n_seqs + kWarps * 32 - 1) / (kWarps * 32) : 0;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(n), (c.n_kv + kWarps - 1) / kWarps, 1);
+  cfg.gridDim = dim3(records + checks, (c.n_kv + kWarps - 1) / kWarps, 1);
   cfg.blockDim = dim3(kWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -349,7 +362,7 @@ cudaError_t launch(K kernel, const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, c, b, r, status);
+  return cudaLaunchKernelEx(&cfg, kernel, c, b, r, status, checks);
 }
 
 }  // namespace

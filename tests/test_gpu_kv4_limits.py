@@ -68,6 +68,30 @@ def test_bad_offsets_are_reported_by_attention(cu, hint):
             ref.assert_close(out[r.start:r.stop], want, tol, f"sequence {s}")
 
 
+FALLS = [([0, 64, 10, 20], 64), ([0, 1000, 0, 16], 1000), ([0, 40, 80, 40], 80), ([0, 64, 20, 64], 64),
+         ([0, 100, 60, 99, 100], 100), ([0] + [500] * 40 + [0, 3], 500), ([0, -40, 5, 6], 64), ([0, 3, 1 << 20, 2], 8),
+         ([0] * 200 + [90, 50, 90], 90)]
+
+
+@pytest.mark.parametrize("cu,rows", FALLS)
+def test_falling_offsets_are_reported_by_append_and_read(cu, rows):
+    """Offsets that fall by more than two records' rows, so that the record numbers of the sequences fall too."""
+    D, page, n_kv = 64, 64, 2
+    n = len(cu) - 1
+    width = -(-(rows + 8) // page)
+    pages = torch.zeros((n * width, n_kv, page * (D + 8)), dtype=torch.uint8, device="cuda")
+    cache = mq.KV4Cache(pages, page, D, F16)
+    table = torch.arange(n * width, dtype=torch.int32, device="cuda").view(n, width)
+    k = torch.randn((rows, n_kv, D), device="cuda").half()
+    lens = ints([8 + max(0, min(b, rows) - max(a, 0)) for a, b in zip(cu, cu[1:])])
+    status = mq.status_tensor()
+    mq.kv4_append(k, k, cache, table, lens, ints(cu), status=status)
+    assert int(status.item()) == 1
+    status.zero_()
+    mq.kv4_read(cache, table, ints(cu), rows, status=status)
+    assert int(status.item()) == 1
+
+
 # ------------------------------------------------------- bytes that no token wrote
 @pytest.mark.parametrize("dtype,s,lo", [(F16, -60000.0, -60000.0), (F16, -5000.0, 0.0), (F16, 60000.0, 60000.0),
                                         (BF16, -1e38, -1e38), (BF16, -3e37, 0.0), (BF16, 1e38, 1e38)])
