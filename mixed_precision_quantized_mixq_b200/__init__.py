@@ -486,6 +486,10 @@ def _kv4_batch(cache: KV4Cache, table, name: str, per_seq, cu, rows: int):
         raise MixqError(1, "the block table must be int32 [n_seqs, width]")
     n, width = table.shape
     at = _kv4_ints(cache, "the block table", table, (n, width))
+    row = table.stride(0) if n > 1 and width else width
+    if row < width:
+        raise MixqError(1, f"rows of the block table overlap (stride {row}, width {width}): an expanded "
+                           "table needs a copy")
     if per_seq is not None:
         per_seq = _kv4_ints(cache, name, per_seq, (n,))
     if cu is not None:
@@ -493,7 +497,7 @@ def _kv4_batch(cache: KV4Cache, table, name: str, per_seq, cu, rows: int):
     elif rows != n:
         raise MixqError(1, f"without row offsets there must be one row per sequence, not {rows} "
                            f"rows for {n} sequences")
-    return n, rows, at, width, max(table.stride(0), width) if n > 1 else width, per_seq, cu
+    return n, rows, at, width, row, per_seq, cu
 
 
 _NOW = contextlib.nullcontext()

@@ -1,0 +1,36 @@
+"""Arguments of the 4-bit KV cache calls that the binding refuses because they could not reach the library as they were
+given: tables whose rows overlap, numbers past 32 bits, a cache that was changed under its descriptor."""
+import pytest
+import torch
+
+import mixed_precision_quantized_mixq_b200 as mq
+
+
+@pytest.fixture()
+def cache():
+    return mq.KV4Cache(torch.zeros((4, 2, 16 * 72), dtype=torch.uint8), 16, 64)
+
+
+def rows(n):
+    return torch.zeros((n, 2, 64)).half()
+
+
+def refused(call):
+    with pytest.raises(mq.MixqError) as e:
+        call()
+    return e.value.status
+
+
+def test_a_table_whose_rows_overlap_is_refused(cache):
+    """One row of a table given to every sequence has stride 0: with the row's width for a stride the call would read
+    past the tensor.  (A cache on the CPU is refused with status 6 when all else is right.)"""
+    lens = torch.ones(3, dtype=torch.int32)
+    flat = torch.zeros(40, dtype=torch.int32)
+    for table in (flat[:4].expand(3, 4), flat.as_strided((3, 4), (2, 1)), flat.as_strided((3, 4), (3, 1)), flat[:1].expand(3, 1)):
+        assert refused(lambda: mq.kv4_append(rows(3), rows(3), cache, table, lens)) == 1
+        assert refused(lambda: mq.kv4_read(cache, table, None, 3)) == 1
+        assert refused(lambda: mq.kv4_attention(rows(3), cache, table, lens)) == 1
+    for table in (flat.as_strided((3, 4), (4, 1)), flat.as_strided((3, 4), (9, 1)), flat.as_strided((3, 0), (0, 1))):
+        assert refused(lambda: mq.kv4_attention(rows(3), cache, table, lens)) == 6
+    assert refused(lambda: mq.kv4_attention(rows(1), cache, flat[:4].expand(1, 4), lens[:1])) == 6
+    assert refused(lambda: mq.kv4_attention(rows(1), cache, flat.as_strided((1, 4), (0, 1)), lens[:1])) == 6
