@@ -26,6 +26,7 @@ STATUS = {0: "MIXQ_OK", 1: "MIXQ_ERR_INVALID_ARG", 2: "MIXQ_ERR_UNSUPPORTED_SHAP
           3: "MIXQ_ERR_MISALIGNED", 4: "MIXQ_ERR_CUDA", 5: "MIXQ_ERR_TIMEOUT",
           6: "MIXQ_ERR_NO_DEVICE"}
 GROUP = 128
+_INT_MAX = 2 ** 31 - 1  # ctypes cuts longer integers without a word
 MIXQ_KV4_F16, MIXQ_KV4_BF16 = 0, 1
 
 _c = ctypes
@@ -585,6 +586,8 @@ def kv4_attention(q, cache: KV4Cache, table, seq_lens, cu_new=None, max_new: int
     scratch from kv4_workspace (default: allocated for the call).  Returns out [rows,
     n_q_heads, head_dim]; a row that sees no key is zeros."""
     torch = cache._torch
+    if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX and 0 <= max_new <= _INT_MAX):
+        raise MixqError(1, "window, sinks and max_new must lie in [0, 2**31 - 1]")
     rows, heads, q_row, q_head = _kv4_rows(cache, "q", q)
     n, _, at, width, table_row, lens, cu = _kv4_batch(cache, table, "seq_lens", seq_lens, cu_new, rows)
     with _on(cache, stream):

@@ -34,3 +34,15 @@ def test_a_table_whose_rows_overlap_is_refused(cache):
         assert refused(lambda: mq.kv4_attention(rows(3), cache, table, lens)) == 6
     assert refused(lambda: mq.kv4_attention(rows(1), cache, flat[:4].expand(1, 4), lens[:1])) == 6
     assert refused(lambda: mq.kv4_attention(rows(1), cache, flat.as_strided((1, 4), (0, 1)), lens[:1])) == 6
+
+
+def test_numbers_past_32_bits_are_refused(cache):
+    """The C call takes 32-bit integers: 2**32 + 5 would arrive as 5."""
+    table, lens = torch.zeros((3, 2), dtype=torch.int32), torch.ones(3, dtype=torch.int32)
+    for name in ("window", "sinks", "max_new"):
+        for value in (2 ** 31, 2 ** 32, 2 ** 32 + 5, -1, -2 ** 32 + 5, 1 << 70):
+            assert refused(lambda: mq.kv4_attention(rows(3), cache, table, lens, **{name: value})) == 1, (name, value)
+        for value in (0, 1, 2 ** 31 - 1):
+            assert refused(lambda: mq.kv4_attention(rows(3), cache, table, lens, **{name: value})) == 6, (name, value)
+    for size in (2 ** 32 + 16, -16, 2 ** 31):
+        assert refused(lambda: mq.KV4Cache(torch.zeros((0, 2, 5), dtype=torch.uint8), size, 64)) == 1
