@@ -558,7 +558,7 @@ def kv4_read(cache: KV4Cache, table, cu_rows, rows: int, first=None, k_out=None,
     return k_out, v_out
 
 
-_kv4_work_bytes: dict = {}  # (device index, head_dim, many rows) -> bytes
+_kv4_work_bytes: dict = {}  # (device index, head_dim, bound on rows) -> bytes
 _KV4_STEP_ROWS = 32
 
 
@@ -567,11 +567,14 @@ def kv4_workspace(cache: KV4Cache, max_rows: int = 0):
 
     max_rows: a bound on new tokens times n_q_heads / n_kv_heads of one sequence (0: none)."""
     torch = cache._torch
-    key = (cache._index, cache.head_dim, not 0 < max_rows <= _KV4_STEP_ROWS)
+    if max_rows < 0:
+        raise MixqError(1, "max_rows must be >= 0")
+    bound = _KV4_STEP_ROWS if 0 < max_rows <= _KV4_STEP_ROWS else 0
+    key = (cache._index, cache.head_dim, bound)
     n = _kv4_work_bytes.get(key)
     if n is None:
         with torch.cuda.device(cache.device):
-            n = lib().mixq_kv4_attention_workspace_size(cache.head_dim, max_rows, 0)
+            n = lib().mixq_kv4_attention_workspace_size(cache.head_dim, bound, 0)
         _kv4_work_bytes[key] = n
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
 

@@ -46,3 +46,33 @@ def test_numbers_past_32_bits_are_refused(cache):
             assert refused(lambda: mq.kv4_attention(rows(3), cache, table, lens, **{name: value})) == 6, (name, value)
     for size in (2 ** 32 + 16, -16, 2 ** 31):
         assert refused(lambda: mq.KV4Cache(torch.zeros((0, 2, 5), dtype=torch.uint8), size, 64)) == 1
+
+
+def test_workspace_sizes_of_any_bound(monkeypatch):
+    """The size for many rows is asked for without a bound, so that neither a bound past 32 bits nor one that is not
+    allowed is remembered as a size of 0 for the calls after it."""
+    asked = []
+
+    class Lib:
+        @staticmethod
+        def mixq_kv4_attention_workspace_size(head_dim, max_rows, num_sms):
+            n = _c_int(max_rows)
+            asked.append(n)
+            return 0 if n < 0 else 1000 if 0 < n <= 32 else 3000
+
+    class Cache:
+        _torch, _index, head_dim, device = torch, 77, 64, torch.device("cpu")
+
+    def _c_int(x):  # as ctypes passes it
+        return (x + 2 ** 31) % 2 ** 32 - 2 ** 31
+
+    import contextlib
+    monkeypatch.setattr(mq, "lib", lambda: Lib)
+    monkeypatch.setattr(mq, "_kv4_work_bytes", {})
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch, "empty", lambda n, **kw: n)
+    for bad in (-1, -2 ** 32 + 5):
+        assert refused(lambda: mq.kv4_workspace(Cache, bad)) == 1
+    for bound, size in ((2 ** 31 + 3, 3000), (2 ** 32 + 3, 3000), (33, 3000), (0, 3000), (32, 1000), (1, 1000)):
+        assert mq.kv4_workspace(Cache, bound) == size, bound
+    assert all(n >= 0 for n in asked)
