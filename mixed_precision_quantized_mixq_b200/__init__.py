@@ -412,6 +412,10 @@ def linear(X, w: PackedWeights, threshold: float = 6.0, status=None, stream=None
 
 
 # ------------------------------------------------------------ 4-bit KV cache
+_KV4_FIXED = frozenset(("pages", "page_size", "head_dim", "dtype", "n_kv_heads", "device", "_torch",
+                        "_index", "_desc", "_ref"))
+
+
 class KV4Cache:
     """A paged cache of K and V rows in 4 bits (layout: mixq_kv4_cache in mixq.h).
 
@@ -435,12 +439,22 @@ class KV4Cache:
         if size != per or (n * heads * size and (by_byte != 1 or (heads > 1 and by_head != per))):
             raise MixqError(1, f"a kv head's part of a page must be {per} contiguous bytes, the "
                                "heads of a page one after another")
-        self.pages, self.page_size, self.head_dim, self.dtype = pages, page_size, head_dim, dtype
-        self.n_kv_heads, self.device = heads, pages.device
-        self._torch, self._index = torch, pages.get_device()  # -1: not on a GPU
-        self._desc = _KV4Desc(pages.data_ptr(), stride if n > 1 else max(1, heads) * per, n,
-                              page_size, heads, head_dim, code)
-        self._ref = ctypes.addressof(self._desc)
+        desc = _KV4Desc(pages.data_ptr(), stride if n > 1 else max(1, heads) * per, n, page_size, heads,
+                        head_dim, code)
+        self.__dict__.update(pages=pages, page_size=page_size, head_dim=head_dim, dtype=dtype,
+                             n_kv_heads=heads, device=pages.device, _torch=torch,
+                             _index=pages.get_device(),  # -1: not on a GPU
+                             _desc=desc, _ref=ctypes.addressof(desc))
+
+    def __setattr__(self, name, value):
+        if name in _KV4_FIXED:  # the descriptor would go on naming the old ones
+            raise AttributeError(f"{name} of a KV4Cache cannot be changed: make another cache")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in _KV4_FIXED:
+            raise AttributeError(f"{name} of a KV4Cache cannot be removed")
+        object.__delattr__(self, name)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int = 128, page_size: int = 64,

@@ -76,3 +76,15 @@ def test_workspace_sizes_of_any_bound(monkeypatch):
     for bound, size in ((2 ** 31 + 3, 3000), (2 ** 32 + 3, 3000), (33, 3000), (0, 3000), (32, 1000), (1, 1000)):
         assert mq.kv4_workspace(Cache, bound) == size, bound
     assert all(n >= 0 for n in asked)
+
+
+def test_a_cache_keeps_what_its_descriptor_says(cache):
+    """The library reads the descriptor made with the cache; pages put in later would not be used, and the old ones
+    might be gone."""
+    for name, value in (("pages", torch.zeros((4, 2, 16 * 72), dtype=torch.uint8)), ("page_size", 32), ("head_dim", 128),
+                        ("dtype", torch.bfloat16), ("n_kv_heads", 1), ("device", torch.device("cuda"))):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, value)
+    with pytest.raises(AttributeError):
+        del cache.pages
+    cache.layer = 3  # what a user adds is the user's
