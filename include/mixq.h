@@ -412,8 +412,8 @@ mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_ro
  * times V's scale in fp16 under a power of two (in two parts of fp16 for an fp16
  * cache); with more rows the weights and V's rows are rounded to fp16 for their
  * product (to bf16 for 16 tokens of a bf16 cache whose V values do not fit fp16).
- * A length below 0 or beyond the table is reported in *status as bad offsets are, at
- * any place of the batch, and counts as 0 or as what the table holds.
+ * A length below 0, beyond the table or above 2^31 - 256 is reported in *status as bad offsets are, at
+ * any place of the batch, and counts as 0, as what the table holds or as that.
  * A row that sees no key is written as zeros; a NaN in a row reaches only those
  * queries that see the row.  A result above the type's largest finite value in size
  * becomes that.  V rows of up to 2^90 in size are safe from overflow in the sums.

@@ -3,6 +3,7 @@
 // kernel launchers, and the thread-local error text.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -653,6 +654,7 @@ mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64
   if (!aligned16(work)) return fail(MIXQ_ERR_MISALIGNED, "work must be 16-byte aligned");
   if ((s = check_device(&a.num_sms)) != MIXQ_OK) return s;
   a.group = n_q_heads / a.c.n_kv;
+  a.room = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(table_width) * cache->page_size, mixq::kKv4MaxKeys));
   a.max_rows = static_cast<int64_t>(!cu ? 1 : max_new > 0 && max_new < n_rows ? max_new : n_rows) * a.group;
   const size_t need = kv4_work(a.c.d, a.max_rows, a.num_sms);
   if (work_bytes < need)

@@ -41,6 +41,10 @@ struct Kv4Rows {  // K and V rows [rows][n_kv][d]; strides in elements
   int64_t k_row, k_head, v_row, v_head;
 };
 
+// Keys of a sequence that attention can see at most: no position, rounded up to a tile of either
+// kernel and a tile further, leaves 32 bits.
+constexpr int kKv4MaxKeys = 0x7fffffff - 255;
+
 struct Kv4AttnArgs {
   Kv4Cache c;
   Kv4Batch b;
@@ -50,6 +54,7 @@ struct Kv4AttnArgs {
   int n_q;    // query heads
   int group;  // n_q / n_kv
   int64_t max_rows;    // bound on a sequence's rows of a kv head (new tokens x group)
+  int room;            // keys that a row of the table has room for, kKv4MaxKeys at most
   int64_t tile_above;  // sequences with more rows than this belong to the tile kernel
   float scale;
   int window, sinks;  // window 0: all keys up to the query's position

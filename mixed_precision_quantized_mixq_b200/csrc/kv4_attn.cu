@@ -81,9 +81,8 @@ __device__ __forceinline__ Seq load_seq(const Kv4AttnArgs &a, int s, bool *wrong
   q.row0 = r.x;
   q.nq = r.y - r.x;
   const int full = __ldg(a.b.lens + s);
-  const int64_t cap = static_cast<int64_t>(a.b.table_width) * a.c.recs_per_page * kKv4Rec;
-  q.len = static_cast<int>(min(static_cast<int64_t>(max(full, 0)), cap));
-  if (wrong) *wrong = bad || full < 0 || full > cap;
+  q.len = min(max(full, 0), a.room);
+  if (wrong) *wrong = bad || full < 0 || full > a.room;
   q.pos0 = full - q.nq;
   const int64_t rows = static_cast<int64_t>(q.nq) * a.group;
   q.tiles = rows > a.tile_above ? 0 : static_cast<int>((rows + R - 1) / R);

@@ -169,10 +169,9 @@ __device__ __forceinline__ Rows load_rows(const Kv4AttnArgs &a, int s) {
   bool bad = false;
   const int2 r = kv4_row_range(a.b, s, &bad);
   const int full = __ldg(a.b.lens + s);
-  const int64_t cap = static_cast<int64_t>(a.b.table_width) * a.c.recs_per_page * kKv4Rec;
-  if ((threadIdx.x & 31) == 0 && (bad || full < 0 || full > cap)) record_error(a.status, kErrInvalidArg);
+  if ((threadIdx.x & 31) == 0 && (bad || full < 0 || full > a.room)) record_error(a.status, kErrInvalidArg);
   q.row0 = r.x;
-  q.len = static_cast<int>(min(static_cast<int64_t>(max(full, 0)), cap));
+  q.len = min(max(full, 0), a.room);
   q.pos0 = full - (r.y - r.x);
   q.rows = (r.y - r.x) * a.group;
   q.blocks = q.rows > a.tile_above ? (q.rows + kRows - 1) / kRows : 0;

@@ -144,3 +144,45 @@ def test_rows_that_reach_the_largest_value(new, D):
     at = [offsets(lens)[s] + lens[s] - rows[s] + i for s in range(2) for i in range(rows[s])]
     want = back[at].repeat_interleave(2, 1).float()
     assert (one.float() - want).abs().max().item() <= 2.0 ** -10 * top
+
+
+# ------------------------------------------------------------------ the last positions
+@pytest.mark.parametrize("dtype,new,group,window,sinks", [
+    (F16, [1, 1], 1, 300, 4), (F16, [1, 1], 1, 5, 0), (BF16, [1, 1], 8, 31, 40), (F16, [40, 3], 2, 300, 4), (BF16, [70, 1], 1, 7, 0),
+    (F16, [3, 200], 1, 130, 200), (BF16, [90, 40], 4, 1, 1)])
+def test_positions_up_to_the_last_that_a_sequence_can_have(dtype, new, group, window, sinks):
+    """Lengths of 2^31 - 256 and a little less under a window, over a table that names few pages again and again; a
+    longer one is reported and cut."""
+    D, page = 64, 1 << 20
+    lens = [2 ** 31 - 256, 2 ** 31 - 256 - 77]
+    g = torch.Generator().manual_seed(55)
+    pages, _, _ = make(55, [page], 1, D, page, dtype, spare=1)
+    table = (torch.arange(2 * 2048).view(2, 2048) * 7 // 5 % 2).int()
+    q = randn(g, (sum(new), group, D), dtype)
+    cu = None if new == [1, 1] else offsets(new)
+    cache, t = mq.KV4Cache(pages.cuda(), page, D, dtype), table.cuda()
+    status = mq.status_tensor()
+    out = mq.kv4_attention(q.cuda(), cache, t, ints(lens), None if cu is None else ints(cu), window=window, sinks=sinks,
+                           status=status)
+    mq.check_status(status)
+    host, at = ref.Pages(pages, page, D, dtype), offsets(new)
+    for s in range(2):
+        # the same keys as a short sequence: its first `sinks` positions, then the last ones
+        from_ = lens[s] - new[s] - window
+        pos = list(range(sinks)) + list(range(from_, lens[s]))
+        k, v = host.rows(table[s], pos, 0)
+        pos = torch.tensor(pos)
+        for i in range(new[s]):
+            p = lens[s] - new[s] + i
+            seen = (pos <= p) & ((pos > p - window) | (pos < sinks))
+            x = q[at[s] + i].double()
+            o = torch.softmax(x @ k[seen].T * D ** -0.5, -1) @ v[seen]
+            # weights and V rows rounded once each to at least the type, and the result: 3 half steps of the largest
+            # |v|, 4 with what the scores and sums lose
+            tol = 4 * torch.finfo(dtype).eps / 2 * v[seen].abs().max().item()
+            assert (out[at[s] + i].double().cpu() - o).abs().max().item() <= tol, (s, i)
+    for bad in (2 ** 31 - 255, 2 ** 31 - 1):
+        status.zero_()
+        mq.kv4_attention(q.cuda(), cache, t, ints([bad, 100]), None if cu is None else ints(cu), window=window, sinks=sinks,
+                         status=status)
+        assert int(status.item()) == 1
