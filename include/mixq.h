@@ -487,6 +487,16 @@ mixq_status mixq_debug_gemm_stall(int M, int N, int K, const int8_t *Xq, const v
                                   uint64_t wait_limit_ns, int32_t *status, void *stream);
 
 /*
+ * Test-only: mixq_kv4_attention (q and out contiguous, head_dim 64, fp16, no window)
+ * by kernels whose pipelines stop, with waits limited to 20 ms.  They must return on their own and write MIXQ_ERR_TIMEOUT to *status; out
+ * then means nothing.
+ */
+mixq_status mixq_debug_kv4_stall(const mixq_kv4_cache *cache, const void *q, void *out,
+                                 int n_q_heads, int n_seqs, int n_rows, const int32_t *table,
+                                 int table_width, const int32_t *seq_lens, const int32_t *cu,
+                                 void *work, size_t work_bytes, int32_t *status, void *stream);
+
+/*
  * Diagnostic: the dense tensor-core rate of this device, measured with the
  * instruction forms the gemm calls use (no page counterpart; it gives the
  * tensor-bound GEMMs a peak taken on the same chip in the same run).  One CTA

@@ -72,6 +72,7 @@ _SIGNATURES = {
     "mixq_debug_max_active_clusters": (_I, [_I, _I, _I, _I, _c.POINTER(_I)]),
     "mixq_debug_unpack_w8": (_I, [_I, _I, _VP, _VP, _VP]),
     "mixq_debug_unpack_w4": (_I, [_I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "mixq_debug_kv4_stall": (_I, [_VP, _VP, _VP, _I, _I, _I, _VP, _I, _VP, _VP, _VP, _SZ, _VP, _VP]),
     "mixq_debug_mma_rate": (_I, [_I, _I, _c.POINTER(_c.c_double), _VP, _VP]),
     "mixq_debug_gemm_stall": (_I, [_I, _I, _I, _VP, _VP, _VP, _VP, _VP, _I, _U64, _VP, _VP]),
 }

@@ -627,13 +627,13 @@ size_t mixq_kv4_attention_workspace_size(int head_dim, int max_rows, int num_sms
   return num_sms > 0 ? kv4_work(head_dim, max_rows ? max_rows : 1 << 30, num_sms) : 0;
 }
 
-mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64_t q_row,
+static mixq_status kv4_attend(const mixq_kv4_cache *cache, const void *q, int64_t q_row,
                                int64_t q_head, void *out, int64_t o_row, int64_t o_head,
                                int n_q_heads, int n_seqs, int n_rows, int max_new,
                                const int32_t *table, int table_width, int64_t table_stride,
                                const int32_t *seq_lens, const int32_t *cu, float scale,
                                int window, int sinks, void *work, size_t work_bytes,
-                               int32_t *status, void *stream) {
+                               bool stall, int32_t *status, void *stream) {
   mixq::Kv4AttnArgs a{};
   mixq_status s = kv4_check(cache, n_seqs, n_rows, table, table_width, table_stride, cu, &a.c, &a.b);
   if (s != MIXQ_OK) return s;
@@ -672,8 +672,33 @@ mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64
   a.sinks = sinks;
   a.work = static_cast<float *>(work);
   a.work_tile = a.work + mixq::kv4_step_workspace(a.c.d, a.num_sms) / sizeof(float);
+  a.stall = stall;
   a.status = status;
   return from_cuda(mixq::launch_kv4_attn(a, static_cast<cudaStream_t>(stream)), "KV4 attention launch");
+}
+
+mixq_status mixq_kv4_attention(const mixq_kv4_cache *cache, const void *q, int64_t q_row,
+                               int64_t q_head, void *out, int64_t o_row, int64_t o_head,
+                               int n_q_heads, int n_seqs, int n_rows, int max_new,
+                               const int32_t *table, int table_width, int64_t table_stride,
+                               const int32_t *seq_lens, const int32_t *cu, float scale,
+                               int window, int sinks, void *work, size_t work_bytes,
+                               int32_t *status, void *stream) {
+  return kv4_attend(cache, q, q_row, q_head, out, o_row, o_head, n_q_heads, n_seqs, n_rows, max_new,
+                    table, table_width, table_stride, seq_lens, cu, scale, window, sinks, work,
+                    work_bytes, false, status, stream);
+}
+
+mixq_status mixq_debug_kv4_stall(const mixq_kv4_cache *cache, const void *q, void *out,
+                                 int n_q_heads, int n_seqs, int n_rows, const int32_t *table,
+                                 int table_width, const int32_t *seq_lens, const int32_t *cu,
+                                 void *work, size_t work_bytes, int32_t *status, void *stream) {
+  if (!cache || !status) return fail(MIXQ_ERR_INVALID_ARG, "cache and status must be non-null");
+  if (cache->head_dim != 64 || cache->dtype != MIXQ_KV4_F16)
+    return fail(MIXQ_ERR_UNSUPPORTED_SHAPE, "head_dim must be 64 and dtype MIXQ_KV4_F16");
+  const int64_t row = static_cast<int64_t>(n_q_heads) * 64;
+  return kv4_attend(cache, q, row, 64, out, row, 64, n_q_heads, n_seqs, n_rows, 0, table, table_width,
+                    table_width, seq_lens, cu, 0.125f, 0, 0, work, work_bytes, true, status, stream);
 }
 
 mixq_status mixq_debug_mma_rate(int kind, int iters, double *ops, int32_t *status, void *stream) {

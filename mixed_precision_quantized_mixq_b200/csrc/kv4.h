@@ -61,6 +61,7 @@ struct Kv4AttnArgs {
   float *work;       // step kernel's parts
   float *work_tile;  // tile kernel's parts
   int num_sms;
+  int stall;  // the variants whose pipelines stop (timeout test; fp16, d 64)
   int32_t *status;
 };
 

@@ -54,7 +54,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr float kNegBig = -1e30f;  // running maximum before the first visible key
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull, kStallWaitNs = 20000000ull;
 constexpr int kUnit = 2;       // records
 constexpr int kUnitKeys = kUnit * kKv4Rec;
 constexpr int kMinQuota = 8;   // units: below one a warp, a cut costs more than it spreads
@@ -170,14 +170,16 @@ struct Smem {
   Place place[2][kWarps];
   uint64_t full[kWarps][SLOTS];
   int ok[kWarps][SLOTS];  // a bit per record
+  int died[kWarps];       // slot * 2 + phase of the unit that did not come
   long long scan[kWarps + 1];
   int found_seq;
   long long found_start;
   long long lo, quota;
 };
 
-// R rows of an item: 16, 8, or 4 that take the 8 columns of a product twice.
-template <typename T, int D, int R, int SLOTS>
+// R rows of an item: 16, 8, or 4 that take the 8 columns of a product twice.  STALL (a test): each
+// warp's first unit is never asked for, and waits are short.
+template <typename T, int D, int R, int SLOTS, bool STALL>
 __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(const Kv4AttnArgs a) {
   constexpr int NT = (R + 7) / 8, WORDS = D / 32, MT = D / 16, REC = kv4_rec_bytes(D);
   constexpr bool BF = Kv4Type<T>::bf16;
@@ -281,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
     pre_i += 32 / kUnit;
   };
   auto issue = [&](int n, int slot) {  // the span's n-th unit
+    if (STALL && n == 0) return;
     const int u = n % (32 / kUnit);
     if (u == 0) {
       place = pre_off;
@@ -315,6 +318,9 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
   for (int i = 0; i < SLOTS; ++i)
     if (w0 + i < w1) issue(i, i);
 
+  // A wait that runs out is the whole warp's: lanes that disagreed about it would part before the
+  // products.  After it the warp waits no more and asks for nothing.
+  constexpr uint64_t wait_ns = STALL ? kStallWaitNs : kWaitNs;
   bool dead = false;
   int slot = 0;
   uint32_t phase = 0;
@@ -415,9 +421,12 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
     // ---- the warp's units of this segment
 #pragma unroll 1
     for (int i = pos; i < seg_end; ++i) {
-      if (!dead && !mbar_wait(&sm.full[warp][slot], phase, kWaitNs)) {
+      if (!dead && __any_sync(0xffffffffu, !mbar_wait(&sm.full[warp][slot], phase, wait_ns))) {
         dead = true;
-        if (lane == 0) record_error(a.status, kErrTimeout);
+        if (lane == 0) {
+          record_error(a.status, kErrTimeout);
+          sm.died[warp] = slot * 2 + phase;
+        }
       }
       const int ok = dead ? 0 : sm.ok[warp][slot];
       const bool whole = i >= from && i < to && ok == 3;
@@ -651,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
         }
       }
       __syncwarp();
-      if (i + SLOTS < w1) issue(i + SLOTS - w0, slot);
+      if (!dead && i + SLOTS < w1) issue(i + SLOTS - w0, slot);
       if (++slot == SLOTS) slot = 0, phase ^= 1;
     }
 
@@ -783,10 +792,15 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
       }
     }
   }
-  // after a wait that ran out, do not leave while copies may still land here
-  if (dead)
-    for (int n = max(w1 - w0 - SLOTS, 0); n < w1 - w0; ++n)
-      mbar_wait(&sm.full[warp][n % SLOTS], n / SLOTS & 1, kWaitNs / 16);
+  // after a wait that ran out, do not leave while copies may still land here: the ring's, from the
+  // slot that did not come on (one that was never asked for costs its limit)
+  if (dead) {
+    slot = sm.died[warp] / 2, phase = sm.died[warp] & 1;
+    for (int n = 0; n < SLOTS; ++n) {
+      mbar_wait(&sm.full[warp][slot], phase, wait_ns / 16);
+      if (++slot == SLOTS) slot = 0, phase ^= 1;
+    }
+  }
 }
 
 // Joins what both kernels cut: first the tile kernel's items (tile_ctas 0: none), then those here.
@@ -801,10 +815,10 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Kv4AttnArgs a,
     kv4_join<D, kMaxRows, 1, T>(a, a.work, ctas, i - tiles, R);
 }
 
-template <typename T, int D, int R>
+template <typename T, int D, int R, bool STALL = false>
 cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
   constexpr int SLOTS = D == 64 ? 5 : R <= 8 ? 3 : 5;  // units in flight: two CTAs fit an SM, or one with 16 rows
-  auto kernel = kv4_attn_kernel<T, D, R, SLOTS>;
+  auto kernel = kv4_attn_kernel<T, D, R, SLOTS, STALL>;
   const int smem = static_cast<int>(sizeof(Smem<D, R, SLOTS>));
   static std::atomic<uint64_t> done{0};
   cudaError_t e = ensure_smem(kernel, smem, done);
@@ -829,6 +843,8 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t pick(const Kv4AttnArgs &a, cudaStream_t stream) {
+  if constexpr (!Kv4Type<T>::bf16 && D == 64)
+    if (a.stall) return launch<T, D, 8, true>(a, stream);
   // the fewest rows per item that take a sequence's rows of a kv head at once; four only where
   // weights have second parts
   if constexpr (!Kv4Type<T>::bf16)

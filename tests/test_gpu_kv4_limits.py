@@ -186,3 +186,24 @@ def test_positions_up_to_the_last_that_a_sequence_can_have(dtype, new, group, wi
         mq.kv4_attention(q.cuda(), cache, t, ints([bad, 100]), None if cu is None else ints(cu), window=window, sinks=sinks,
                          status=status)
         assert int(status.item()) == 1
+
+
+# ------------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("new", [[1, 1, 1]])
+def test_stalled_attention_times_out_with_status(new):
+    """The test variants, whose work never comes, end by themselves with the status; calls after them are right."""
+    D, page, n_kv, heads = 64, 16, 2, 4
+    lens = [5000, 2100, 900]
+    pages, table, g = make(56, lens, n_kv, D, page, F16)
+    cache, t, cu, n = mq.KV4Cache(pages.cuda(), page, D, F16), table.cuda(), ints(offsets(new)), ints(lens)
+    q = randn(g, (sum(new), heads, D), F16).cuda()
+    before = mq.kv4_attention(q, cache, t, n, cu)
+    work, out, status = mq.kv4_workspace(cache), torch.empty_like(q), mq.status_tensor()
+    for _ in range(2):
+        status.zero_()
+        mq._check(mq.lib().mixq_debug_kv4_stall(cache._ref, q.data_ptr(), out.data_ptr(), heads, 3, sum(new), t.data_ptr(),
+                                                t.shape[1], n.data_ptr(), cu.data_ptr(), work.data_ptr(), work.nbytes,
+                                                status.data_ptr(), torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        assert int(status.item()) == 5
+    assert torch.equal(mq.kv4_attention(q, cache, t, n, cu, work=work), before)

@@ -88,3 +88,14 @@ def test_a_cache_keeps_what_its_descriptor_says(cache):
     with pytest.raises(AttributeError):
         del cache.pages
     cache.layer = 3  # what a user adds is the user's
+
+
+def test_stall_call_refusals():
+    desc = mq._KV4Desc(0x10000, 2 * 16 * 72, 4, 16, 2, 64, 0)
+    import ctypes
+    call = lambda d, status: mq.lib().mixq_debug_kv4_stall(  # noqa: E731
+        None if d is None else ctypes.addressof(d), 0x20000, 0x30000, 2, 1, 1, 0x40000, 4, 0x50000, None, 0x60000, 1 << 30, status, None)
+    assert call(None, 0x70000) == 1 and call(desc, None) == 1
+    for change in ({"head_dim": 128}, {"dtype": 1}):
+        other = mq._KV4Desc(0x10000, 2 * 16 * 136, 4, 16, 2, change.get("head_dim", 64), change.get("dtype", 0))
+        assert call(other, 0x70000) == 2
