@@ -63,7 +63,7 @@ constexpr int kSeqChunk = 64;  // sequences the search for a CTA's part looks at
 constexpr int kTurn = 2;       // what the turn to an item costs, in key tiles (four prompts: 196 us with 1, 189 with 2, 197 with 3)
 constexpr int kMinTiles = 4;   // key tiles per part: below, joining costs more than the cut spreads
 constexpr float kNegBig = -1e30f;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull, kStallWaitNs = 20000000ull;
 
 constexpr int kItems = 8;      // items the walk may be ahead
 
@@ -99,6 +99,7 @@ struct TileSmem {
 };
 
 // Bounded wait; once one has run out, none waits any more and the CTA winds up.
+template <bool STALL>
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile int *dead, int32_t *status) {
   if (mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = globaltimer_ns();
@@ -106,7 +107,7 @@ __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, volatile in
 #pragma unroll 1
     for (int i = 0; i < 16; ++i)
       if (mbar_try_wait(bar, parity)) return;
-    if (globaltimer_ns() - t0 > kWaitNs) {
+    if (globaltimer_ns() - t0 > (STALL ? kStallWaitNs : kWaitNs)) {
       *dead = 1;
       record_error(status, kErrTimeout);
     }
@@ -252,7 +253,8 @@ using Desc = Kv4Join;
 
 __host__ __device__ constexpr size_t slot_floats(int d) { return kv4_slot_floats(kRows, d); }
 
-template <typename T, int D>
+// STALL (a test): the CTA's second tile of V never arrives, and waits are short.
+template <typename T, int D, bool STALL>
 __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs a) {
   using S = TileSmem<D>;
   using X = Kv4Type<T>;
@@ -422,15 +424,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       const float2 f = from_f32x2(sum);
       qsum = f.x + f.y;
     };
-    wait(&sm.item_full[0], 0, &sm.dead, a.status);
-    if (sm.item[0].n > 0) {
+    wait<STALL>(&sm.item_full[0], 0, &sm.dead, a.status);
+    // an item after a wait that ran out may be half written, and its rows lie anywhere
+    auto there = [&](const Item &x) { return !__any_sync(0xffffffffu, x.n == 0 || sm.dead); };
+    if (there(sm.item[0])) {
       fetch_q(sm.item[0]);
       have_q(sm.item[0]);
     }
 #pragma unroll 1
     for (int it = 0;; ++it) {
       const Item &x = sm.item[it % kItems], &nx = sm.item[(it + 1) % kItems];  // x has arrived already
-      if (__any_sync(0xffffffffu, x.n == 0 || sm.dead)) break;  // the lanes leave together
+      if (!there(x)) break;  // the lanes leave together
       const int n = i ? x.n : x.n0;  // of this row tile
       const bool active = i * 128 < x.rows;
       uint64_t la = f32x2(0.f, 0.f), lb = la;
@@ -451,20 +455,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         for (int j = 0; j < n; ++j) {
           const int st = (jt + j) & 3;
           if (ahead) {  // the keys are there when the scores are
-            wait(&sm.s_full[i], jn & 1, &sm.dead, a.status);
+            wait<STALL>(&sm.s_full[i], jn & 1, &sm.dead, a.status);
             ahead = false;
           }
-          wait(&sm.par_full[st], ((jt + j) >> 2) & 1, &sm.dead, a.status);
+          wait<STALL>(&sm.par_full[st], ((jt + j) >> 2) & 1, &sm.dead, a.status);
           const float4 *kp = sm.kp[st];
           const uint2 hid = *reinterpret_cast<const uint2 *>(sm.hidden[st]);
           const int k0 = (x.t0 + j + (x.t0 + j >= x.sinks ? x.skip : 0)) * kKeys;
           const bool whole = ((hid.x | hid.y) & 0x01010101u) == 0 && k0 + kKeys <= sm.sight[r].z &&
                              (a.window <= 0 || k0 > sm.sight[r].w - a.window || k0 + kKeys <= a.sinks);
-          wait(&sm.s_full[i], (jn + j) & 1, &sm.dead, a.status);
+          wait<STALL>(&sm.s_full[i], (jn + j) & 1, &sm.dead, a.status);
           tc_fence_after();
           if (j + 1 == n) {  // the last scores are there, so the operand tile is free for the next rows
-            wait(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
-            if (nx.n > 0) fetch_q(nx);
+            wait<STALL>(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
+            if (there(nx)) fetch_q(nx);
           }
           union Chunk {
             uint32_t u[32];
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             la = mul_f32x2(la, al2);
             lb = mul_f32x2(lb, al2);
             if (j > 0) {
-              wait(&sm.o_full[i], (jn + j - 1) & 1, &sm.dead, a.status);
+              wait<STALL>(&sm.o_full[i], (jn + j - 1) & 1, &sm.dead, a.status);
               tc_fence_after();
 #pragma unroll 1
               for (int x = 0; x < D / 16; ++x) {
@@ -582,11 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         jn += n;
       } else {
         ahead = true;
-        wait(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
-        if (nx.n > 0) fetch_q(nx);
+        wait<STALL>(&sm.item_full[(it + 1) % kItems], (it + 1) / kItems & 1, &sm.dead, a.status);
+        if (there(nx)) fetch_q(nx);
       }
       jt += x.n;
-      if (nx.n > 0) have_q(nx);
+      if (there(nx)) have_q(nx);
       // ---- the result.  Column c of O is dim 2c, column D/2 + c dim 2c + 1.
       if (active) {
         const float2 l0 = from_f32x2(la), l1 = from_f32x2(lb);
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         T *op = static_cast<T *>(a.out) + (x.row0 + static_cast<int64_t>(qi)) * a.o_row +
                 (static_cast<int64_t>(x.head) * a.group + (rr - qi * a.group)) * a.o_head;
         float *part = slots + (2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0)) * slot_floats(D);
-        wait(&sm.o_full[i], (jn - 1) & 1, &sm.dead, a.status);
+        wait<STALL>(&sm.o_full[i], (jn - 1) & 1, &sm.dead, a.status);
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -629,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[it % kItems]);
     }
+    cp_async_wait_all();  // rows that were asked for before a wait ran out
   } else if (warp < 24) {
     // -------------------------------------------------------------- unpack
     // One record a warp and tile: its K codes and pairs (warps 8-15), its V rows (16-23).
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
     bool end = false;   // no more tiles
     auto load = [&](int j) {
       const int b = j >> 2;
-      if ((j & 3) == 0) wait(&sm.src_full[b & 1], b >> 1 & 1, &sm.dead, a.status);
+      if ((j & 3) == 0) wait<STALL>(&sm.src_full[b & 1], b >> 1 & 1, &sm.dead, a.status);
       const int64_t off = sm.src[b & 1][(j & 3) * 8 + rw];
       end = __any_sync(0xffffffffu, off == -3 || sm.dead);  // the lanes leave together
       if ((j & 3) == 3) {
@@ -680,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         const int st = j & 1;
         const float2 own = kv4_pair<BF>(pr);
         const bool both = finite(own);
-        if (j >= 2) wait(&sm.k_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
+        if (j >= 2) wait<STALL>(&sm.k_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
         if (lane < 16) {
           float *kp = reinterpret_cast<float *>(&sm.kp[j & 3][rw * 8 + lane / 2]) + (lane & 1);
           kp[0] = both ? own.x * sl2 : 0.f;
@@ -727,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         const int st = j & 1;
         const float2 own = kv4_pair<BF>(pr);
         const bool both = finite(own);
-        if (j >= 2) wait(&sm.v_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
+        if (j >= 2) wait<STALL>(&sm.v_empty[st], (j / 2 - 1) & 1, &sm.dead, a.status);
         // transposed: tile row = dim (2b at b, 2b + 1 at D/2 + b), 64 keys per 128-byte atom
         // (s, lo) of this lane's tokens 2t, 2t+1 and 2t+8, 2t+9
         const uint32_t use = both ? pr : 0u;
@@ -788,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_full[st]);
+        if (lane == 0 && !(STALL && j == 1)) mbar_arrive(&sm.v_full[st]);
         load(j + 1);
       }
     }
@@ -841,26 +846,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
         const bool turn = j + 1 >= n;  // the next scores are another item's
         if (turn) {
           const int slot = (n ? it + 1 : it) % kItems;
-          wait(&sm.item_full[slot], (n ? it + 1 : it) / kItems & 1, &sm.dead, a.status);
+          wait<STALL>(&sm.item_full[slot], (n ? it + 1 : it) / kItems & 1, &sm.dead, a.status);
           next_n = sm.item[slot].n;
           next_n0 = sm.item[slot].n0;
           next_tiles = __any_sync(0xffffffffu, next_n == 0 || sm.dead) ? 0 : sm.item[slot].rows > 128 ? 2 : 1;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
         }
-        if (row_tiles) wait(&sm.v_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
+        if (row_tiles) wait<STALL>(&sm.v_full[jt & 1], (jt / 2) & 1, &sm.dead, a.status);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (i < row_tiles && (i || j < n0)) {
-            wait(&sm.p_full[i], p_phase >> i & 1, &sm.dead, a.status);
+            wait<STALL>(&sm.p_full[i], p_phase >> i & 1, &sm.dead, a.status);
             p_phase ^= 1u << i;
             tc_fence_after();
             pv(i, jt, j > 0);
           }
-          if (i == 0 && next_tiles) wait(&sm.k_full[(jt + 1) & 1], ((jt + 1) / 2) & 1, &sm.dead, a.status);
+          if (i == 0 && next_tiles) wait<STALL>(&sm.k_full[(jt + 1) & 1], ((jt + 1) / 2) & 1, &sm.dead, a.status);
           if (i < next_tiles && (i || (turn ? 0 : j + 1) < next_n0)) {
             if (turn) {
-              wait(&sm.q_full[i], q_phase >> i & 1, &sm.dead, a.status);
+              wait<STALL>(&sm.q_full[i], q_phase >> i & 1, &sm.dead, a.status);
               q_phase ^= 1u << i;
             }
             tc_fence_after();
@@ -889,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
       // Items and the places of records, four tiles (32 lanes) at a time, ahead of the other roles.
       int it = 0, pj = 0;
       auto publish = [&](bool end) {
-        if (it >= kItems) wait(&sm.item_empty[it % kItems], (it / kItems - 1) & 1, &sm.dead, a.status);
+        if (it >= kItems) wait<STALL>(&sm.item_empty[it % kItems], (it / kItems - 1) & 1, &sm.dead, a.status);
         const int n = end ? 0 : w.t1 - w.t0, first = w.block * kRows;
         const int seen0 = min(w.q.len, w.q.pos0 + (first + min(127, w.rows() - 1)) / a.group + 1);
         const bool less = n > 1 && w.k.key0(w.t1 - 1) >= seen0;
@@ -938,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             off = page * a.c.page_stride + (static_cast<int64_t>(head) * a.c.recs_per_page + (rec - slot * a.c.recs_per_page)) * REC;
           }
         }
-        if (b >= 2) wait(&sm.src_empty[b & 1], (b / 2 - 1) & 1, &sm.dead, a.status);
+        if (b >= 2) wait<STALL>(&sm.src_empty[b & 1], (b / 2 - 1) & 1, &sm.dead, a.status);
         sm.src[b & 1][lane] = off;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.src_full[b & 1]);
@@ -956,9 +961,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool STALL = false>
 cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t stream) {
-  auto kernel = kv4_tile_kernel<T, D>;
+  auto kernel = kv4_tile_kernel<T, D, STALL>;
   const int smem = static_cast<int>(sizeof(TileSmem<D>));
   static std::atomic<uint64_t> done{0};
   cudaError_t e = ensure_smem(kernel, smem, done);
@@ -983,6 +988,7 @@ size_t kv4_tile_workspace(int d, int num_sms) {
 }
 
 cudaError_t launch_kv4_tile(const Kv4AttnArgs &a, cudaStream_t stream) {
+  if (a.stall && !a.c.bf16 && a.c.d == 64) return launch<__half, 64, true>(a, stream);
   if (a.c.bf16)
     return a.c.d == 128 ? launch<__nv_bfloat16, 128>(a, stream) : launch<__nv_bfloat16, 64>(a, stream);
   return a.c.d == 128 ? launch<__half, 128>(a, stream) : launch<__half, 64>(a, stream);

@@ -189,9 +189,10 @@ def test_positions_up_to_the_last_that_a_sequence_can_have(dtype, new, group, wi
 
 
 # ------------------------------------------------------------------- waits that run out
-@pytest.mark.parametrize("new", [[1, 1, 1]])
+@pytest.mark.parametrize("new", [[1, 1, 1], [1, 40, 1], [300, 129, 64]])
 def test_stalled_attention_times_out_with_status(new):
-    """The test variants, whose work never comes, end by themselves with the status; calls after them are right."""
+    """The test variants, whose work never comes, end by themselves with the status, on the kernel for few rows, on both
+    and on the one for many; calls after them are right."""
     D, page, n_kv, heads = 64, 16, 2, 4
     lens = [5000, 2100, 900]
     pages, table, g = make(56, lens, n_kv, D, page, F16)
