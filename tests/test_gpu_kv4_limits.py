@@ -188,6 +188,59 @@ def test_positions_up_to_the_last_that_a_sequence_can_have(dtype, new, group, wi
         assert int(status.item()) == 1
 
 
+# ------------------------------------------------------------ many blocks, long contexts
+@pytest.mark.parametrize("dtype,D", [(F16, 64), (BF16, 128)])
+def test_more_sequences_than_one_look_takes(dtype, D):
+    """150 and 70 sequences on both kernels, some without rows or keys: the search for a CTA's part goes over several
+    groups of 64."""
+    g = torch.Generator().manual_seed(57)
+    for n, most in ((150, 40), (70, 70)):
+        new = torch.randint(0, most, (n,), generator=g).tolist()
+        new[::7] = [0] * len(new[::7])
+        new[3::11] = [1] * len(new[3::11])
+        lens = [m + int(x) for m, x in zip(new, torch.randint(0, 30, (n,), generator=g))]
+        lens[5] = 0
+        attend(57, lens, new, 3, 1, D, 16, dtype, window=20 if n == 70 else 0, sinks=2)
+
+
+def test_more_blocks_of_rows_than_one_look_takes():
+    """A sequence with 9600 and one with 17000 rows of a kv head, 38 and 67 blocks of 256, between short ones."""
+    attend(58, [20, 140, 3], [5, 150, 1], 64, 1, 64, 16, F16)
+    attend(59, [170, 9], [170, 2], 100, 1, 64, 16, BF16, window=50)
+
+
+@pytest.mark.parametrize("rows,heads", [(1, 1), (1, 8), (1, 16), (40, 2)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("length", [2000, 131071])
+def test_error_over_long_contexts(rows, heads, dtype, length):
+    """The error's RMS against what rounding the exact result gives, which is one unit: u = 0.72 2^-11 / sqrt(3) of the
+    result's RMS for fp16 (half a step, evenly spread, over a binade), 8 u for bf16.  V is N(0, 1), its rows' lo about
+    -2.6, so the codes' part of a row has a mean square of 1 + 2.6^2 = 7.8 against the row's 1.
+    Few rows: the weights go in as two fp16 parts for fp16 (2^-22: nothing), and sums lose less than a unit: 1.5 units in
+    all; one part would be sqrt(1 + 7.8) = 3.  For bf16 one part is sqrt(7.8) / 8 of a unit and cut-off sums half of one:
+    sqrt(1 + 0.12 + 0.25) = 1.17, held to 1.25.
+    Many rows: weights and V rows rounded once each to fp16 add a unit each for fp16, sqrt(3) = 1.73, held to 1.9; for
+    bf16 1/8 of a unit each, 1.02, held to 1.1."""
+    D, page = 128, 128
+    g = torch.Generator().manual_seed(60)
+    n = -(-length // page)
+    cache = mq.KV4Cache.empty(n, 1, D, page, dtype)
+    table = torch.randperm(n, generator=g).int()[None]
+    k, v, q = randn(g, (length, 1, D), dtype), randn(g, (length, 1, D), dtype), randn(g, (rows, heads, D), dtype)
+    k[..., ::16] *= 6
+    t, lens = table.cuda(), ints([length])
+    mq.kv4_append(k.cuda(), v.cuda(), cache, t, lens, ints([0, length]))
+    out = mq.kv4_attention(q.cuda(), cache, t, lens, ints([0, rows])).double().cpu()
+    kk, vv = ref.Pages(cache.pages.cpu(), page, D, dtype).rows(table[0], range(length), 0)
+    z = q.double().flatten(0, 1) @ kk.T * D ** -0.5
+    first = length - rows + torch.arange(rows).repeat_interleave(heads)
+    z.masked_fill_(torch.arange(length) > first[:, None], float("-inf"))
+    want = (torch.softmax(z, -1) @ vv).view(rows, heads, D)
+    unit = (want.to(dtype).double() - want).square().mean().sqrt()
+    most = (1.5 if dtype == F16 else 1.25) if rows * heads <= 32 else (1.9 if dtype == F16 else 1.1)
+    assert ((out - want).square().mean().sqrt() / unit).item() <= most
+
+
 # ------------------------------------------------------------------- waits that run out
 @pytest.mark.parametrize("new", [[1, 1, 1], [1, 40, 1], [300, 129, 64]])
 def test_stalled_attention_times_out_with_status(new):
