@@ -26,7 +26,6 @@ STATUS = {0: "MIXQ_OK", 1: "MIXQ_ERR_INVALID_ARG", 2: "MIXQ_ERR_UNSUPPORTED_SHAP
           3: "MIXQ_ERR_MISALIGNED", 4: "MIXQ_ERR_CUDA", 5: "MIXQ_ERR_TIMEOUT",
           6: "MIXQ_ERR_NO_DEVICE"}
 GROUP = 128
-_INT_MAX = 2 ** 31 - 1  # ctypes cuts longer integers without a word
 MIXQ_KV4_F16, MIXQ_KV4_BF16 = 0, 1
 
 _c = ctypes
@@ -442,10 +441,11 @@ class KV4Cache:
                                "heads of a page one after another")
         desc = _KV4Desc(pages.data_ptr(), stride if n > 1 else max(1, heads) * per, n, page_size, heads,
                         head_dim, code)
-        self.__dict__.update(pages=pages, page_size=page_size, head_dim=head_dim, dtype=dtype,
-                             n_kv_heads=heads, device=pages.device, _torch=torch,
-                             _index=pages.get_device(),  # -1: not on a GPU
-                             _desc=desc, _ref=ctypes.addressof(desc))
+        d = self.__dict__
+        d["pages"], d["page_size"], d["head_dim"], d["dtype"] = pages, page_size, head_dim, dtype
+        d["n_kv_heads"], d["device"] = heads, pages.device
+        d["_torch"], d["_index"] = torch, pages.get_device()  # -1: not on a GPU
+        d["_desc"], d["_ref"] = desc, ctypes.addressof(desc)
 
     def __setattr__(self, name, value):
         if name in _KV4_FIXED:  # the descriptor would go on naming the old ones
@@ -604,7 +604,7 @@ def kv4_attention(q, cache: KV4Cache, table, seq_lens, cu_new=None, max_new: int
     scratch from kv4_workspace (default: allocated for the call).  Returns out [rows,
     n_q_heads, head_dim]; a row that sees no key is zeros."""
     torch = cache._torch
-    if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX and 0 <= max_new <= _INT_MAX):
+    if (window | sinks | max_new) >> 31:  # below 0 or past a C int, which ctypes cuts without a word
         raise MixqError(1, "window, sinks and max_new must lie in [0, 2**31 - 1]")
     rows, heads, q_row, q_head = _kv4_rows(cache, "q", q)
     n, _, at, width, table_row, lens, cu = _kv4_batch(cache, table, "seq_lens", seq_lens, cu_new, rows)
