@@ -411,7 +411,8 @@ mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_ro
  * grouped heads) per kv head take V's codes and pairs as they are too, weights
  * times V's scale in fp16 under a power of two (in two parts of fp16 for an fp16
  * cache); with more rows the weights and V's rows are rounded to fp16 for their
- * product (to bf16 for 16 tokens of a bf16 cache whose V values do not fit fp16).
+ * product (to bf16 for 16 tokens of a bf16 cache whose V values, or the bytes behind
+ * the last token, do not fit fp16).
  * A length below 0, beyond the table or above 2^31 - 256 is reported in *status as bad offsets are, at
  * any place of the batch, and counts as 0, as what the table holds or as that.
  * A row that sees no key is written as zeros; a NaN in a row reaches only those
@@ -420,7 +421,9 @@ mixq_status mixq_kv4_read(const mixq_kv4_cache *cache, void *k_out, int64_t k_ro
  *   q, out   [n_rows][n_q_heads][head_dim], strides in elements, multiples of 8;
  *            16-byte aligned; out must not overlap q
  *   max_new  a bound on cu[s+1] - cu[s], or 0 for none: it picks the kernel, the
- *            results are right whatever it says
+ *            results are right whatever it says.  A step of single tokens that
+ *            has cu should give 1: a call that may hold chunks takes its single
+ *            tokens 16 rows at a time and, with more than 32 rows, a launch more
  *   window >= 0 (0: no window), sinks >= 0 (first tokens that stay visible)
  *   work     device scratch of mixq_kv4_attention_workspace_size bytes, 16-byte
  *            aligned; its contents before and after mean nothing, and calls that

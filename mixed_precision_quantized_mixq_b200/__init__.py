@@ -599,7 +599,8 @@ def kv4_attention(q, cache: KV4Cache, table, seq_lens, cu_new=None, max_new: int
     """Causal attention of new tokens over the cache (which holds their K and V already).
 
     q [rows, n_q_heads, head_dim]; table, seq_lens and cu_new as in kv4_append; max_new: a bound
-    on the new rows of one sequence, if known (a hint); scale: default head_dim ** -0.5;
+    on the new rows of one sequence, if known (a hint; give 1 for a step that has cu_new, which is
+    else run as a batch that may hold chunks); scale: default head_dim ** -0.5;
     window > 0: only the last `window` positions and the first `sinks` ones are seen; work:
     scratch from kv4_workspace (default: allocated for the call).  Returns out [rows,
     n_q_heads, head_dim]; a row that sees no key is zeros."""

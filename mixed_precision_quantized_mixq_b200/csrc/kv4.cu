@@ -17,8 +17,8 @@
 // What they measured (B200): 107 MB of rows of six 7B prompts written in 34.5 us
 // (3.9 TB/s with the codes; 1860 instructions a record and head, 73 % of the issue
 // slots: the instructions bound it, not HBM) and read back in 27 (5.1 TB/s); eight
-// prefixes of up to 16384 tokens, 389 MB, read in 69 (5.7 TB/s, 86 % of the measured
-// copy rate).  A fourth block per SM (64 registers) brought 2 us of the
+// prefixes of up to 16384 tokens, 389 MB, read in 65 (6.0 TB/s, 91 % of the measured
+// copy rate; issue slots 72 %).  A fourth block per SM (64 registers) brought 2 us of the
 // write, asking for the page beside the rows 2 more.
 #include <cuda_runtime.h>
 

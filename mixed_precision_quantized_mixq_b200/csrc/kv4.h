@@ -71,7 +71,11 @@ cudaError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &b, const Kv4Rows 
                             int32_t *status, cudaStream_t stream);
 size_t kv4_step_workspace(int d, int num_sms);
 size_t kv4_tile_workspace(int d, int num_sms);
-constexpr int kKv4TileAbove = 32;  // more rows (new tokens x group) of a kv head than this: tile kernel
+// More rows (new tokens x group) of a kv head than this: tile kernel.  16 sequences of 4096 tokens, 64 / 8
+// heads of 128, fp16, us by the step / the tile kernel: 16 rows 60 / 107, 32 rows 80 / 109, 40 rows
+// 92 / 109, 48 rows 105 / 109, 64 rows 132 / 110; bf16 57 / 111 up to 116 / 113; D 64 41 / 95 up to
+// 95 / 97.  One sequence alone: 35 / 35 at 16 rows, 31 / 37 at 64.
+constexpr int kKv4TileAbove = 32;
 // Decode steps and small row counts (kv4_attn.cu), many rows (kv4_tile.cu); the
 // first launches the second where it is needed, and the join of what both cut (kv4_join.cuh).
 cudaError_t launch_kv4_attn(Kv4AttnArgs a, cudaStream_t stream);

@@ -28,7 +28,7 @@
 //
 // What it measured (B200, warm launches, us against the bytes at the measured copy
 // rate): 16 sequences of up to 4096 tokens, 32 / 32 heads, fp16 50 (30); 64 of up to
-// 8192, 64 / 8 heads, bf16 87 (54); two of 131071, 64 / 8 heads, fp16 82 (44); a
+// 8192, 64 / 8 heads, bf16 85 (54); two of 131071, 64 / 8 heads, fp16 82 (44); a
 // window of 4096 over 16 sequences, 32 / 8 heads 35 (11).  With the arithmetic left
 // out the second takes 67, with the copies left out about as long as whole: about 260
 // instructions a record and warp, 88 of them masks and shifts, at 0.55 issues a
@@ -609,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, R <= 8 ? 2 : 1) kv4_attn_kernel(cons
           products(std::true_type{});
         // Codes are all positive, so what the products lose does not cancel against lo's part of the
         // row, and the mean over a long context is small beside both.  A bf16 result is rounded far
-        // enough to hide that.  For fp16 caches
+        // enough to hide that (16384 tokens: 1.01 to 1.08 of the rounding's own error; 131071: 1.09).
+        // For fp16 caches
         //   weights go in as two fp16 parts (22 bits); with four rows the columns 4..7 hold the second
         //   parts, else they are a product of their own (8 % of the kernel);
         //   a row of sevens among the codes sums what the same instructions make of the weights, which
@@ -846,7 +847,8 @@ cudaError_t pick(const Kv4AttnArgs &a, cudaStream_t stream) {
   if constexpr (!Kv4Type<T>::bf16 && D == 64)
     if (a.stall) return launch<T, D, 8, true>(a, stream);
   // the fewest rows per item that take a sequence's rows of a kv head at once; four only where
-  // weights have second parts
+  // weights have second parts (16 sequences of up to 4096, 32 / 32 heads of 128, one row each, by items
+  // of 4 / 8 / 16 rows: fp16 50 / 54 / 80 us, bf16 - / 49 / 70)
   if constexpr (!Kv4Type<T>::bf16)
     if (a.max_rows <= 4) return launch<T, D, 4>(a, stream);
   return a.max_rows <= 8 ? launch<T, D, 8>(a, stream) : launch<T, D, 16>(a, stream);

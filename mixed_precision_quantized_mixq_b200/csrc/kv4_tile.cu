@@ -29,9 +29,12 @@
 //
 // The running maximum moves only when a score passes it by 2^8, so O (in TMEM) is
 // rarely rescaled, and by whole powers of two, which is exact; P carries 2^6 more so
-// that fp16 keeps 11 bits down to 2^-20 of the row's largest weight.
+// that fp16 keeps 11 bits down to 2^-20 of the row's largest weight.  Weights and V are rounded to 11
+// bits each: an error of 3.5e-4 of the result for fp16, where rounding the result alone gives 2.1e-4.
+// Weights as two fp16 parts, the second in the TMEM columns that their scores leave, brought 2.9e-4
+// and cost a fifth (four prompts 187 -> 226 us, windowed chunks 99 -> 113): left out.
 //
-// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 773 us, 689
+// What bounds it (B200, 1024 tokens over 15360, 64 / 8 heads of 128, bf16: 772 us, 690
 // TFLOP/s, 42 % of the measured matrix peak; four ragged prompts of up to 2048 tokens,
 // 32 heads: 188 us, 356 TFLOP/s): no unit alone.  A pair of row tiles takes about 6100
 // cycles a key tile; the matrix products and the exponentials need 2048 each, the
@@ -60,7 +63,10 @@ constexpr int kThreads = 896;  // softmax 0-7, K 8-15, V 16-23, MMA 24, walk 25 
 constexpr int kRows = kKv4TileRows;  // query rows per CTA
 constexpr int kKeys = 128;     // keys per tile
 constexpr int kSeqChunk = 64;  // sequences the search for a CTA's part looks at together
-constexpr int kTurn = 2;       // what the turn to an item costs, in key tiles (four prompts: 196 us with 1, 189 with 2, 197 with 3)
+// What the turn to an item costs, in key tiles.  With 1 / 2 / 3, us: four prompts of 32 heads, D 128
+// 193 / 187 / 194 in fp16 and 206 / 200 / 207 in bf16, D 64 155 / 159 / 164 and 165 / 169 / 174; 70B
+// chunk 775 / 771 / 774; windowed chunks, D 64 99 / 99 / 101, D 128 117 / 115 / 117.
+constexpr int kTurn = 2;
 constexpr int kMinTiles = 4;   // key tiles per part: below, joining costs more than the cut spreads
 constexpr float kNegBig = -1e30f;
 constexpr uint64_t kWaitNs = 2000000000ull, kStallWaitNs = 20000000ull;
@@ -564,7 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnArgs
             tmem_st16(tm_s(i) + lanes + c * 16, p);
           }
           tmem_st_wait();
-          if (BF && __builtin_expect((hid.x | hid.y) & 0x02020202u, 0)) {  // weights of bf16 products
+          // Weights of bf16 products.  Which records those are shows only here: the conversion beside the
+          // exponentials would be in every tile's code.  Rounded from fp16 they are off by 2^-12 more beside
+          // bf16's own 2^-9.
+          if (BF && __builtin_expect((hid.x | hid.y) & 0x02020202u, 0)) {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const uint32_t w = (c < 2 ? hid.x : hid.y) >> ((c & 1) * 16);
